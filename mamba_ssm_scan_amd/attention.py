@@ -1,0 +1,300 @@
+"""The attention layer of a hybrid stack: rotary positions, a paged 8-bit cache, attention over it.
+
+torch tensors in, the C entry points of include/m3_attn.h called, as in `binding`: argument marshalling only,
+outputs and workspaces allocated with torch on the call's stream, no other implementation behind it.
+
+    cache = attention.KVCache.empty(num_pages, 64, kv_heads, head_dim)          # int8; or torch.float8_e4m3fn
+    inv_freq, mscale = attention.rope_frequencies(head_dim)
+    kv_len += 1                                                                  # int32 [batch], on the device
+    q = cache.append(k, v, kv_len, pages, q=q, inv_freq=inv_freq)                # one new token a sequence
+    o = cache.attend(q, kv_len, pages)
+
+A prompt, or a ragged batch, gives its row offsets `cu_q` and the longest `max_q`.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import binding
+from .binding import check
+
+M3_KV_INT8, M3_KV_FP8 = 0, 1
+BLOCK = 16  # tokens that share a scale, per head
+FORMATS = {torch.int8: M3_KV_INT8, torch.float8_e4m3fn: M3_KV_FP8}
+
+# every symbol include/m3_attn.h declares
+EXPORTS = ["m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend", "m3_kv_attend_workspace_size"]
+
+_vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+
+
+class M3KvCache(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("num_pages", _i64), ("page_size", _i32),
+                ("heads", _i32), ("headdim", _i32), ("format", _i32)]
+
+
+class M3KvBatch(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("tokens", _i64), ("max_pages", _i64), ("max_q", _i64), ("max_kv", _i64),
+                ("cu_q", _vp), ("kv_len", _vp), ("pages", _vp)]
+
+
+class M3Rows(ctypes.Structure):
+    _fields_ = [("p", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class M3Rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", _vp), ("rot", _i32), ("interleaved", _i32), ("mscale", _f32)]
+
+
+_ready = None
+
+
+def _lib():
+    global _ready
+    if _ready is None:
+        lib = binding.load()
+        cache, batch, rows, rot = (ctypes.POINTER(t) for t in (M3KvCache, M3KvBatch, M3Rows, M3Rotary))
+        lib.m3_rope.argtypes = [rows, rows, _i64, _i32, _i32, ctypes.c_int, _vp, rot, _i32, _vp]
+        lib.m3_kv_append.argtypes = [cache, batch, rows, rows, rows, rows, _i32, ctypes.c_int, rot, _vp]
+        lib.m3_kv_read.argtypes = [cache, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, ctypes.c_int, _vp]
+        lib.m3_kv_attend.argtypes = [cache, batch, rows, _vp, _vp, _i32, ctypes.c_int, _f32, _i32, _i64, _vp, _sz, _vp]
+        lib.m3_kv_attend_workspace_size.argtypes = [cache, batch, _i32, ctypes.c_int, _i32, _i64]
+        lib.m3_kv_attend_workspace_size.restype = _sz
+        for name in ("m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend"):
+            getattr(lib, name).restype = ctypes.c_int
+        _ready = lib
+    return _ready
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """The device and stream of a call: its allocations belong to that stream, so their memory is not handed on early."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _same(t: torch.Tensor, name: str, device, dtype, shape=None):
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _dense(t: torch.Tensor, name: str, device, dtype, shape=None):
+    _same(t, name, device, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t: torch.Tensor, name: str, device, dtype, shape=None) -> M3Rows:
+    """[tokens][heads][dim] rows where they lie: the entries of a head contiguous, any other strides."""
+    _same(t, name, device, dtype, shape)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][dim]")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the entries of a head must be contiguous")
+    return M3Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _device_of(t: torch.Tensor, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _rotary(inv_freq, device, interleaved, mscale) -> M3Rotary:
+    _dense(inv_freq, "inv_freq", device, torch.float32)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot / 2]")
+    return M3Rotary(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), float(mscale))
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[str] = None, factor: float = 1.0,
+                     trained_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq [rot / 2] fp32, mscale): f_i = base^(-2i / rot), for contexts `factor` times the trained length.
+
+    scaling None: as they are. "linear": f_i / factor (positions squeezed into the trained range). "base": the base
+    grown by factor^(rot / (rot - 2)), so the slowest pair is squeezed by the factor and the fastest hardly. "bands":
+    pairs that turn more than beta_fast times within trained_len keep f_i, those below beta_slow turns take
+    f_i / factor, a linear blend between, and mscale = 0.1 ln(factor) + 1.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and >= 2, got {rot}")
+    if scaling not in (None, "linear", "base", "bands"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling is not None and not factor >= 1.0:
+        raise ValueError(f"factor must be >= 1, got {factor}")
+    if scaling == "base" and rot == 2:
+        raise ValueError("scaling 'base' needs rot > 2")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    f = torch.tensor([base ** (-2.0 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if trained_len < 1 or not beta_fast > beta_slow:
+            raise ValueError("scaling 'bands' needs trained_len >= 1 and beta_fast > beta_slow")
+        turns = trained_len * f / (2.0 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    return f.to(torch.float32).to(device), mscale
+
+
+def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None,
+         stream=None):
+    """m3_rope: x [tokens][heads][dim] (bf16 or fp32) turned by positions [tokens] int32; returns out.
+
+    backward: the transposed map (dL/dx from x = dL/dy). out may be x itself.
+    """
+    dev = _device_of(x, "x")
+    code = binding._io_code(x.dtype)
+    rx = _rows(x, "x", dev, x.dtype)
+    T, H, D = x.shape
+    _dense(positions, "positions", dev, torch.int32, (T,))
+    rot = _rotary(inv_freq, dev, interleaved, mscale)
+    lib = _lib()
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        ry = _rows(out, "out", dev, x.dtype, (T, H, D))
+        check(lib.m3_rope(rx, ry, T, H, D, code, positions.data_ptr(), rot, int(bool(backward)), s))
+    return out
+
+
+class KVCache:
+    """A paged cache of keys and values in 8 bits, one scale per 16 tokens and head (the layout of m3_kv_cache).
+
+    k [pages][heads][page_size / 16][16][dim] and v [pages][heads][page_size / 16][dim][16], int8 or float8_e4m3fn;
+    k_scale, v_scale [pages][heads][page_size / 16] fp32. Sequences, page tables and lengths are the caller's: `pages`
+    [batch][max_pages] int32 names each sequence's pages in order, `kv_len` [batch] int32 its tokens with the call's
+    new ones in (0: an idle slot). Rows of the call's tokens follow one another, `cu_q` [batch + 1] int32 where a
+    sequence may have other than one, `max_q` at least the longest.
+    """
+
+    def __init__(self, k, v, k_scale, v_scale):
+        dev = _device_of(k, "k")
+        if k.dtype not in FORMATS:
+            raise TypeError(f"k must be int8 or float8_e4m3fn, got {k.dtype}")
+        if k.dim() != 5 or k.shape[3] != BLOCK:
+            raise ValueError("k must be [pages][heads][page_size / 16][16][dim]")
+        P, H, S, _, D = k.shape
+        _dense(k, "k", dev, k.dtype)
+        _dense(v, "v", dev, k.dtype, (P, H, S, D, BLOCK))
+        _dense(k_scale, "k_scale", dev, torch.float32, (P, H, S))
+        _dense(v_scale, "v_scale", dev, torch.float32, (P, H, S))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.heads, self.head_dim, self.page_size = dev, H, D, S * BLOCK
+        self._c = M3KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, S * BLOCK, H, D,
+                            FORMATS[k.dtype])
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, dtype=torch.int8, device="cuda"):
+        """A cache that holds nothing yet (its memory is not cleared: a block is written whole when it begins)."""
+        if page_size < BLOCK or page_size % BLOCK:
+            raise ValueError(f"page_size must be a power of two >= {BLOCK}, got {page_size}")
+        sub = page_size // BLOCK
+        new = lambda *shape: torch.empty(shape, dtype=torch.int8, device=device).view(dtype)  # noqa: E731
+        scale = lambda: torch.empty((num_pages, heads, sub), dtype=torch.float32, device=device)  # noqa: E731
+        return cls(new(num_pages, heads, sub, BLOCK, head_dim), new(num_pages, heads, sub, head_dim, BLOCK), scale(),
+                   scale())
+
+    def _batch(self, tokens, kv_len, pages, cu_q, max_q, max_kv) -> M3KvBatch:
+        dev = self.device
+        _dense(kv_len, "kv_len", dev, torch.int32)
+        _dense(pages, "pages", dev, torch.int32)
+        if kv_len.dim() != 1 or pages.dim() != 2 or pages.shape[0] != kv_len.shape[0]:
+            raise ValueError("kv_len must be [batch] and pages [batch][max_pages]")
+        b = kv_len.shape[0]
+        if cu_q is not None:
+            _dense(cu_q, "cu_q", dev, torch.int32, (b + 1,))
+        elif tokens != b:
+            raise ValueError(f"{tokens} rows for {b} sequences need cu_q")
+        cap = pages.shape[1] * self.page_size
+        return M3KvBatch(b, tokens, pages.shape[1], int(max_q), cap if max_kv is None else int(max_kv),
+                         None if cu_q is None else cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr())
+
+    def append(self, k, v, kv_len, pages, *, cu_q=None, max_q: int = 1, q=None, q_out=None, inv_freq=None,
+               interleaved: bool = False, mscale: float = 1.0, stream=None):
+        """m3_kv_append: k, v [tokens][heads][dim] (bf16 or fp32) into the cache, the keys turned by inv_freq (None:
+        as they are). With q [tokens][q_heads][dim], returns it turned by the same positions."""
+        dev, T = self.device, k.shape[0]
+        code = binding._io_code(k.dtype)
+        shape = (T, self.heads, self.head_dim)
+        rk, rv = _rows(k, "k", dev, k.dtype, shape), _rows(v, "v", dev, k.dtype, shape)
+        b = self._batch(T, kv_len, pages, cu_q, max_q, None)
+        rot = None if inv_freq is None else _rotary(inv_freq, dev, interleaved, mscale)
+        lib = _lib()
+        with _on(dev, stream) as s:
+            rq = ro = None
+            qh = 0
+            if q is not None:
+                rq, qh = _rows(q, "q", dev, k.dtype), q.shape[1]
+                if q_out is None:
+                    q_out = torch.empty((T, qh, self.head_dim), dtype=k.dtype, device=dev)
+                _same(q, "q", dev, k.dtype, (T, qh, self.head_dim))
+                ro = _rows(q_out, "q_out", dev, k.dtype, (T, qh, self.head_dim))
+            elif q_out is not None:
+                raise ValueError("q_out without q")
+            check(lib.m3_kv_append(self._c, b, rk, rv, rq, ro, qh, code, rot, s))
+        return q_out
+
+    def read(self, first, count, pages, max_count: int, dtype=torch.bfloat16, stream=None):
+        """m3_kv_read: the values held at positions first[i] .. first[i] + count[i] - 1 of each sequence, as k, v
+        [batch][max_count][heads][dim]; rows past count are zero."""
+        dev = self.device
+        code = binding._io_code(dtype)
+        _dense(first, "first", dev, torch.int32)
+        b = first.numel()
+        _dense(count, "count", dev, torch.int32, (b,))
+        _dense(pages, "pages", dev, torch.int32)
+        if first.dim() != 1 or pages.dim() != 2 or pages.shape[0] != b:
+            raise ValueError("first and count must be [batch] and pages [batch][max_pages]")
+        if max_count < 0:
+            raise ValueError(f"max_count {max_count} < 0")
+        lib = _lib()
+        with _on(dev, stream) as s:
+            k, v = (torch.empty((b, max_count, self.heads, self.head_dim), dtype=dtype, device=dev) for _ in range(2))
+            check(lib.m3_kv_read(self._c, b, first.data_ptr(), count.data_ptr(), pages.data_ptr(), pages.shape[1],
+                                 int(max_count), k.data_ptr(), v.data_ptr(), code, s))
+        return k, v
+
+    def attend(self, q, kv_len, pages, *, cu_q=None, max_q: int = 1, max_kv: Optional[int] = None,
+               scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None, lse=False, stream=None):
+        """m3_kv_attend: q [tokens][q_heads][dim] over the cache; returns out, or (out, lse) with lse=True.
+
+        scale: 1 / sqrt(dim) unless given. causal: a row sees the keys up to its own position; window > 0: only the
+        last `window` of them. A row that sees nothing gives 0 (and lse -inf). max_kv: at least the largest kv_len,
+        the page table's room unless given (a tighter bound saves empty workgroups).
+        """
+        dev = self.device
+        code = binding._io_code(q.dtype)
+        rq = _rows(q, "q", dev, q.dtype)
+        T, H, D = q.shape
+        if D != self.head_dim:
+            raise ValueError(f"q has heads of {D} entries, the cache of {self.head_dim}")
+        b = self._batch(T, kv_len, pages, cu_q, max_q, max_kv)
+        sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
+        lib = _lib()
+        with _on(dev, stream) as s:
+            if out is None:
+                out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
+            _dense(out, "out", dev, q.dtype, (T, H, D))
+            l = torch.empty((T, H), dtype=torch.float32, device=dev) if lse else None
+            n = lib.m3_kv_attend_workspace_size(self._c, b, H, code, int(bool(causal)), int(window))
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            check(lib.m3_kv_attend(self._c, b, rq, out.data_ptr(), l.data_ptr() if lse else None, H, code, sc,
+                                   int(bool(causal)), int(window), ws.data_ptr() if n else None, n, s))
+        return (out, l) if lse else out

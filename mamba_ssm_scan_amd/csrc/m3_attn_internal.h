@@ -1,0 +1,79 @@
+// m3_attn_internal.h -- what the attention layer's entry points (m3_attn_host.cpp)
+// hand to its kernel launchers. Not part of the public ABI.
+#pragma once
+#include "../../include/m3_attn.h"
+#include "m3_internal.h"
+
+namespace m3 {
+
+struct RopeArgs {
+    const void* x;
+    void* y;
+    int64_t x_tok, x_head, y_tok, y_head;  // strides, elements
+    int64_t tokens;
+    int32_t heads, D;
+    m3_dtype io;
+    const int32_t* positions;
+    m3_rotary rot;
+    int32_t backward;
+    bool wide;  // pointers and strides take 16-byte accesses
+    hipStream_t stream;
+};
+hipError_t launch_rope(const RopeArgs& a);
+
+struct AppendArgs {
+    m3_kv_cache c;
+    m3_kv_batch b;
+    m3_rows k, v, q, q_out;  // q.p NULL: no queries
+    int32_t q_heads;
+    m3_dtype io;
+    m3_rotary rot;  // inv_freq NULL: no rotation
+    bool wide;
+    hipStream_t stream;
+};
+hipError_t launch_kv_append(const AppendArgs& a);
+
+struct ReadArgs {
+    m3_kv_cache c;
+    int64_t batch, max_pages, max_count;
+    const int32_t* first;
+    const int32_t* count;
+    const int32_t* pages;
+    void* k_out;
+    void* v_out;
+    m3_dtype io;
+    hipStream_t stream;
+};
+hipError_t launch_kv_read(const ReadArgs& a);
+
+// How the rows and keys of an attend call are cut: a tile of `rows` (row, head of
+// a group) pairs of one sequence and key head, its keys in tiles of 64, `splits`
+// workgroups along them with `split_tiles` tiles each.
+struct AttendPlan {
+    int32_t rows;         // rows of a tile
+    int64_t row_tiles;    // per sequence
+    int32_t splits;
+    int64_t split_tiles;
+    size_t o_off, ml_off, total;  // workspace: parts [splits][tokens][q_heads][D], (max, sum) pairs
+};
+struct AttendArgs {
+    m3_kv_cache c;
+    m3_kv_batch b;
+    m3_rows q;
+    void* out;
+    float* lse;
+    int32_t q_heads;
+    m3_dtype io;
+    float scale;
+    int32_t causal;
+    int64_t window;
+    AttendPlan plan;
+    void* workspace;
+    bool wide;
+    hipStream_t stream;
+};
+AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
+                       int64_t window);
+hipError_t launch_kv_attend(const AttendArgs& a);
+
+}  // namespace m3

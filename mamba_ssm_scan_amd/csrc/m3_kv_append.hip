@@ -1,0 +1,328 @@
+// m3_kv_append.hip -- new keys and values into the paged 8-bit cache, the keys
+// (and the queries) turned on the way; and the cache's values read back.
+//
+// Per touched block of 16 tokens and head: s' = max(old ? s : 0, max|new| / Q),
+// code = nearest(x / s'). Memory-bound: the new rows are read once and their
+// codes written once, old codes are read only in the block a sequence was in the
+// middle of. A workgroup takes one block of one sequence; the (cos, sin) of its
+// tokens are formed once (fp64) and shared by its jobs: K and V of each cache
+// head and the query heads, one job a wave at a time, dealt over blockIdx.y when
+// the blocks alone would leave the chip idle (single tokens).
+//
+// A job's rows go through the wave's own LDS rows in fp32: the maximum has to be
+// known before the first code, a rotation pairs entries of different lanes, and
+// V's codes lie transposed ([entry][token], so that attention reads 16 tokens of
+// an entry with one load). Waves never wait for each other after the angles.
+#include <algorithm>
+
+#include "m3_attn_device.h"
+#include "m3_attn_internal.h"
+
+namespace m3 {
+namespace {
+
+struct AppendDev {
+    m3_kv_cache c;
+    m3_kv_batch b;
+    m3_rows k, v, q, qo;
+    int q_heads, D, half, interleaved, shift, nblk;
+    float mscale;
+    const float* inv_freq;
+};
+
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ unsigned wave_umax(unsigned v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v = max(v, unsigned(__shfl_xor(int(v), m)));
+    return v;
+}
+__device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Rows lo .. hi - 1 of a job into LDS (fp32), turned where cs is given; returns
+// the lane's largest magnitude as bits (above any finite one for inf and NaN).
+template <typename T, bool WIDE>
+__device__ __forceinline__ unsigned gather(const AppendDev& a, const T* src, int64_t tok, int lo, int hi, float* rows,
+                                           const float2* cs, int lane) {
+    const int D = a.D, per = D / 8;
+    const int rot = cs ? 2 * a.half : 0;
+    unsigned top = 0;
+    for (int e = lane; e < (hi - lo) * per; e += 64) {
+        const int s = e / per, d = 8 * (e - s * per);
+        float v[8];
+        load8<WIDE>(src + s * tok + d, v);
+        float* o = rows + (lo + s) * D + d;
+        *reinterpret_cast<floatx4*>(o) = floatx4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<floatx4*>(o + 4) = floatx4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = d + j >= rot ? max(top, mag(v[j])) : top;
+    }
+    wave_fence();
+    if (rot) {
+        for (int e = lane; e < (hi - lo) * a.half; e += 64) {
+            const int s = e / a.half, i = e - s * a.half;
+            const int i0 = a.interleaved ? 2 * i : i, i1 = a.interleaved ? 2 * i + 1 : i + a.half;
+            float* o = rows + (lo + s) * D;
+            float u = o[i0], v = o[i1];
+            const float2 w = cs[(lo + s) * a.half + i];
+            turn(u, v, w.x, w.y);
+            o[i0] = u;
+            o[i1] = v;
+            top = max(top, max(mag(u), mag(v)));
+        }
+        wave_fence();
+    }
+    return top;
+}
+
+// The scale of a block from its old one and the largest new magnitude.
+struct Scale {
+    float s, inv;  // stored scale; 1 / s, or 0 where nothing can be held (s 0 or not finite)
+};
+template <bool FP8>
+__device__ __forceinline__ Scale new_scale(float old, unsigned top) {
+    const unsigned m = max(mag(old), mag(__uint_as_float(top) * (1.f / Code<FP8>::kTop)));
+    Scale r{__uint_as_float(m), 0.f};
+    if (m >= 0x7f800000u)
+        r.s = __uint_as_float(0x7fc00000u);
+    else if (m < 0x00800000u)  // below the normal numbers: 1 / s could overflow
+        r.s = 0.f;
+    else
+        r.inv = 1.f / r.s;
+    return r;
+}
+
+// 16 codes from 16 fp32 values at p, stride st, times f
+template <bool FP8>
+__device__ __forceinline__ u32x4 codes16(const float* p, int st, float f) {
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        w[j] = Code<FP8>::enc4(p[(4 * j) * st] * f, p[(4 * j + 1) * st] * f, p[(4 * j + 2) * st] * f,
+                               p[(4 * j + 3) * st] * f);
+    return w;
+}
+template <bool FP8>
+__device__ __forceinline__ u32x4 recode16(u32x4 w, float ratio) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float v[4];
+        Code<FP8>::dec4(w[j], v);
+        w[j] = Code<FP8>::enc4(v[0] * ratio, v[1] * ratio, v[2] * ratio, v[3] * ratio);
+    }
+    return w;
+}
+
+template <typename T, bool FP8, bool WIDE>
+__global__ void append_kernel(AppendDev a) {
+    extern __shared__ __align__(16) float lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int64_t i = blockIdx.x / a.nblk;
+    const Seq q = seq_of(a.b, i);
+    const int64_t before = int64_t(q.held) - q.n;  // position of the sequence's first row (negative: not stored)
+    const int64_t blk = (before >> 4) + int(blockIdx.x % a.nblk);
+    const int lo = int(max(before - 16 * blk, int64_t(0)));
+    const int hi = int(min(int64_t(q.held) - 16 * blk, int64_t(16)));  // slots lo .. hi - 1 are new
+    if (hi <= lo) return;                          // (the workgroup as a whole)
+    const int64_t row = q.row0 + (16 * blk + lo - before);
+
+    float* rows = lds + wave * 16 * a.D;
+    float2* cs = nullptr;
+    if (a.inv_freq) {
+        cs = reinterpret_cast<float2*>(lds + waves * 16 * a.D);
+        for (int e = threadIdx.x; e < (hi - lo) * a.half; e += blockDim.x) {
+            const int s = e / a.half, p = e - s * a.half;
+            float c, sn;
+            cos_sin(int32_t(16 * blk + lo + s), a.inv_freq[p], double(a.mscale), &c, &sn);
+            cs[(lo + s) * a.half + p] = float2{c, sn};
+        }
+        __syncthreads();
+    }
+    const int H = a.c.heads, D = a.D;
+    const int64_t at = block_at(a.b.pages + i * a.b.max_pages, a.b.max_pages, a.c.num_pages, a.shift, H, blk);
+    const bool begun = lo > 0 && blk * 16 < before;
+    for (int j = blockIdx.y * waves + wave; j < 2 * H + a.q_heads; j += gridDim.y * waves) {
+        if (j >= 2 * H) {  // a query head
+            const int h = j - 2 * H;
+            const T* src = static_cast<const T*>(a.q.p) + row * a.q.token_stride + h * a.q.head_stride;
+            T* dst = static_cast<T*>(a.qo.p) + row * a.qo.token_stride + h * a.qo.head_stride;
+            gather<T, WIDE>(a, src, a.q.token_stride, lo, hi, rows, cs, lane);
+            for (int e = lane; e < (hi - lo) * (D / 8); e += 64) {
+                const int s = e / (D / 8), d = 8 * (e - s * (D / 8));
+                store8<WIDE>(dst + s * a.qo.token_stride + d, rows + (lo + s) * D + d);
+            }
+            wave_fence();
+            continue;
+        }
+        if (at < 0) continue;
+        const bool is_v = j >= H;
+        const int h = is_v ? j - H : j;
+        const m3_rows& r = is_v ? a.v : a.k;
+        const int64_t slot = at + (int64_t(h) << a.shift);
+        float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + slot;
+        u32x4* code = reinterpret_cast<u32x4*>(static_cast<char*>(is_v ? a.c.v : a.c.k) + slot * 16 * D);
+        const float old = begun ? *scale : 0.f;
+        const T* src = static_cast<const T*>(r.p) + row * r.token_stride + h * r.head_stride;
+        const unsigned top = wave_umax(gather<T, WIDE>(a, src, r.token_stride, lo, hi, rows, is_v ? nullptr : cs, lane));
+        const Scale ns = new_scale<FP8>(old, top);
+        const bool grown = __float_as_uint(ns.s) != __float_as_uint(old);
+        const float ratio = ns.inv == 0.f ? 0.f : old * ns.inv;
+        const bool none = ns.inv == 0.f;
+        if (is_v) {
+            // 16 slots of one entry a lane; old slots keep their byte unless the scale grew
+            for (int d = lane; d < D; d += 64) {
+                u32x4 w = begun ? code[d] : u32x4{0, 0, 0, 0};
+                if (begun && grown) w = none ? u32x4{0, 0, 0, 0} : recode16<FP8>(w, ratio);
+                const u32x4 f = none ? u32x4{0, 0, 0, 0} : codes16<FP8>(rows + d, D, ns.inv);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int l = min(max(lo - 4 * b, 0), 4), u = min(max(hi - 4 * b, 0), 4);
+                    const unsigned below = l == 4 ? ~0u : (1u << (8 * l)) - 1u;
+                    const unsigned upto = u == 4 ? ~0u : (1u << (8 * u)) - 1u;
+                    w[b] = (w[b] & below) | (f[b] & upto & ~below);
+                }
+                code[d] = w;
+            }
+        } else {
+            // a row of D codes a slot: the new ones, and all 16 where the block begins or the scale grew
+            const int s0 = begun && !grown ? lo : 0, s1 = begun && !grown ? hi : 16, per = D / 16;
+            for (int e = lane; e < (s1 - s0) * per; e += 64) {
+                const int s = s0 + e / per, d = e % per;
+                u32x4 w{0, 0, 0, 0};
+                if (!none && s < lo)
+                    w = begun ? recode16<FP8>(code[s * per + d], ratio) : w;
+                else if (!none && s < hi)
+                    w = codes16<FP8>(rows + s * D + 16 * d, 1, ns.inv);
+                code[s * per + d] = w;
+            }
+        }
+        if (lane == 0) *scale = ns.s;
+        wave_fence();
+    }
+}
+
+template <typename T, bool FP8>
+hipError_t launch_append(const AppendArgs& a) {
+    AppendDev d{a.c, a.b, a.k, a.v, a.q, a.q_out, a.q.p ? a.q_heads : 0, a.c.headdim, a.rot.rot / 2,
+                a.rot.interleaved, __builtin_ctz(unsigned(a.c.page_size / 16)), int((a.b.max_q + 14) / 16 + 1),
+                a.rot.mscale, a.rot.inv_freq};
+    const int64_t blocks = a.b.batch * d.nblk;
+    const int waves = a.c.headdim <= 128 ? 4 : 2;  // LDS rows and angles within 64 KiB
+    const int jobs = 2 * a.c.heads + d.q_heads;
+    // as many slices of the jobs as leave about 4 workgroups a CU
+    const int slices = int(std::max<int64_t>(1, std::min<int64_t>((jobs + waves - 1) / waves, 1024 / blocks)));
+    const size_t lds = size_t(waves) * 16 * a.c.headdim * 4 + (a.rot.inv_freq ? size_t(16) * d.half * 8 : 0);
+    const dim3 grid{unsigned(blocks), unsigned(slices)}, block{unsigned(64 * waves)};
+    if (a.wide)
+        hipLaunchKernelGGL((append_kernel<T, FP8, true>), grid, block, lds, a.stream, d);
+    else
+        hipLaunchKernelGGL((append_kernel<T, FP8, false>), grid, block, lds, a.stream, d);
+    return hipGetLastError();
+}
+
+struct ReadDev {
+    m3_kv_cache c;
+    const int32_t* first;
+    const int32_t* count;
+    const int32_t* pages;
+    void* k_out;
+    void* v_out;
+    int64_t max_pages, max_count;
+    int D, shift, nblk;
+};
+
+// One block of positions of one sequence a workgroup, K or V of a head a wave.
+// K: 16 entries of a row a lane. V: two entries' 16 tokens a lane, stored as
+// pairs, so that a wave's store is whole lines of a row.
+template <typename T, bool FP8>
+__global__ __launch_bounds__(256) void read_kernel(ReadDev a) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = blockIdx.x / a.nblk;
+    const int64_t first = a.first[i], count = min(int64_t(max(a.count[i], 0)), a.max_count);
+    const int64_t blk = (first >> 4) + int(blockIdx.x % a.nblk);
+    const int64_t j0 = 16 * blk - first;  // output row of slot 0
+    const int H = a.c.heads, D = a.D;
+    const int64_t at = block_at(a.pages + i * a.max_pages, a.max_pages, a.c.num_pages, a.shift, H, blk);
+    for (int j = blockIdx.y * 4 + wave; j < 2 * H; j += gridDim.y * 4) {
+        const bool is_v = j >= H;
+        const int h = is_v ? j - H : j;
+        const int64_t slot = at + (int64_t(h) << a.shift);
+        T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + ((i * a.max_count + j0) * H + h) * int64_t(D);
+        const char* code = static_cast<const char*>(is_v ? a.c.v : a.c.k) + slot * 16 * D;
+        const bool any = at >= 0 && j0 < count && 16 * blk + 16 > 0;
+        const float sc = any ? (is_v ? a.c.v_scale : a.c.k_scale)[slot] : 0.f;
+        if (!is_v) {
+            const int per = D / 16;
+            for (int e = lane; e < 16 * per; e += 64) {
+                const int s = e / per, d = 16 * (e - s * per);
+                const int64_t r = j0 + s;
+                if (r < 0 || r >= a.max_count) continue;
+                float v[16];
+                const bool live = any && r < count;
+                const u32x4 w = live ? *reinterpret_cast<const u32x4*>(code + s * D + d) : u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int b = 0; b < 4; ++b) Code<FP8>::dec4(w[b], v + 4 * b);
+#pragma unroll
+                for (int b = 0; b < 16; ++b) v[b] = live ? v[b] * sc : 0.f;
+                T* o = out + s * int64_t(H) * D + d;
+                store8<true>(o, v);
+                store8<true>(o + 8, v + 8);
+            }
+        } else {
+            for (int d = 2 * lane; d < D; d += 128) {
+                u32x4 w0{0, 0, 0, 0}, w1{0, 0, 0, 0};
+                if (any) {
+                    w0 = *reinterpret_cast<const u32x4*>(code + d * 16);
+                    w1 = *reinterpret_cast<const u32x4*>(code + d * 16 + 16);
+                }
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float v0[4], v1[4];
+                    Code<FP8>::dec4(w0[b], v0);
+                    Code<FP8>::dec4(w1[b], v1);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int64_t r = j0 + 4 * b + s;
+                        if (r < 0 || r >= a.max_count) continue;
+                        const bool live = any && r < count;
+                        const float x = live ? v0[s] * sc : 0.f, y = live ? v1[s] * sc : 0.f;
+                        T* o = out + (4 * b + s) * int64_t(H) * D + d;
+                        if constexpr (sizeof(T) == 2)
+                            *reinterpret_cast<unsigned*>(o) = pack_bf16(x, y);
+                        else
+                            *reinterpret_cast<float2*>(o) = float2{x, y};
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <typename T, bool FP8>
+hipError_t launch_read(const ReadArgs& a) {
+    ReadDev d{a.c, a.first, a.count, a.pages, a.k_out, a.v_out, a.max_pages, a.max_count, a.c.headdim,
+              __builtin_ctz(unsigned(a.c.page_size / 16)), int((a.max_count + 14) / 16 + 1)};
+    const int64_t blocks = a.batch * d.nblk;
+    const int slices = int(std::max<int64_t>(1, std::min<int64_t>((2 * a.c.heads + 3) / 4, 2048 / blocks)));
+    const dim3 grid{unsigned(blocks), unsigned(slices)};
+    hipLaunchKernelGGL((read_kernel<T, FP8>), grid, dim3(256), 0, a.stream, d);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const AppendArgs& a) {
+    const bool fp8 = a.c.format == M3_KV_FP8;
+    if (a.io == M3_BF16) return fp8 ? launch_append<bf16_t, true>(a) : launch_append<bf16_t, false>(a);
+    return fp8 ? launch_append<float, true>(a) : launch_append<float, false>(a);
+}
+
+hipError_t launch_kv_read(const ReadArgs& a) {
+    const bool fp8 = a.c.format == M3_KV_FP8;
+    if (a.io == M3_BF16) return fp8 ? launch_read<bf16_t, true>(a) : launch_read<bf16_t, false>(a);
+    return fp8 ? launch_read<float, true>(a) : launch_read<float, false>(a);
+}
+
+}  // namespace m3
