@@ -1,0 +1,173 @@
+// m3_attend_common.h -- what the two attention kernels share (m3_kv_attend.hip: few
+// rows a sequence; m3_kv_attend_tile.hip: many). Device code only.
+#pragma once
+#include "m3_attn_device.h"
+#include "m3_attn_internal.h"
+
+namespace m3 {
+
+// A call as the kernels take it.
+struct AttendDev {
+    m3_kv_cache c;
+    m3_kv_batch b;
+    m3_rows q;
+    void* out;
+    float* lse;
+    float* part_o;   // [splits][tokens][q_heads][D], sums in the part's unit
+    float* part_ml;  // [splits][tokens][q_heads][2], log2 of the part's unit and its sum
+    int q_heads, group, D, shift, rows;
+    float scale2;    // scale * log2(e)
+    int causal;
+    int64_t window, row_tiles, split_tiles;
+    int splits;
+    bool wide;
+    int64_t blocks;  // workgroups with work (the grid may hold a few more)
+};
+
+hipError_t launch_attend_tile(const AttendDev& d, hipStream_t s);
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kTile = 64;  // keys of a tile
+
+__device__ __forceinline__ floatx4 mfma_f16(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+__device__ __forceinline__ floatx4 mfma(u32x4 a, u32x4 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+
+// Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see.
+struct Span {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0) {
+    const int r1 = min(r0 + a.rows, s.n * a.group) - 1;
+    const int64_t base = int64_t(s.held) - s.n;
+    int64_t hi = min(int64_t(s.held), a.b.max_kv), lo = 0;
+    if (a.causal) hi = min(hi, base + r1 / a.group + 1);
+    if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);
+    if (hi <= lo) return Span{0, 0};
+    return Span{lo / kTile, (hi + kTile - 1) / kTile};
+}
+
+// 8 entries of a query row as MFMA operands: one bf16 part, or three that add
+// up to the fp32 value.
+template <typename T>
+struct Parts;
+template <>
+struct Parts<bf16_t> {
+    static constexpr int kN = 1;  // parts of a query
+    static constexpr int kV = 1;  // parts of a probability
+    __device__ __forceinline__ static void load(const bf16_t* p, bool wide, u32x4* f) {
+        if (wide) {
+            f[0] = *reinterpret_cast<const u32x4*>(p);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[0][j] = unsigned(p[2 * j].bits) | unsigned(p[2 * j + 1].bits) << 16;
+        }
+    }
+};
+__device__ __forceinline__ void split3(float lo, float hi, unsigned* w) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        w[k] = pack_bf16(lo, hi);
+        lo -= __uint_as_float(w[k] << 16);
+        hi -= __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+template <>
+struct Parts<float> {
+    static constexpr int kN = 3;
+    static constexpr int kV = 2;
+    __device__ __forceinline__ static void load(const float* p, bool wide, u32x4* f) {
+        float v[8];
+        if (wide)
+            load8<true>(p, v);
+        else
+            load8<false>(p, v);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            unsigned w[3];
+            split3(v[2 * j], v[2 * j + 1], w);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) f[k][j] = w[k];
+        }
+    }
+};
+
+// Probabilities. p' = 2^(s + log2 vs - M + kUp): the score s (log2), the scale vs of
+// the key's V block, and the row's running reference M >= s + log2 vs - 8 of all keys
+// so far, so that sum p' code is the output's numerator and sum p' / vs its
+// denominator, in units of 2^(M - kUp). p' is at most 2^15 and is rounded to fp16 for
+// the product with V: 11 bits where bf16 would have 8, and what falls under fp16's
+// smallest number is below 2^-31 of the largest p'. fp32 rows add the rest of each p'
+// as a second fp16 part. The denominator takes p' in fp32 (its 1 / vs may differ
+// widely between blocks). A block whose scale is 0 holds zeros: it counts as 2^-60.
+constexpr float kUp = 7.f, kSlack = 8.f;
+struct VScale {
+    float log2, inv;
+};
+__device__ __forceinline__ VScale v_scale(float vs) {
+    vs = vs == 0.f ? 8.673617379884035e-19f : vs;
+    return VScale{__builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
+}
+__device__ __forceinline__ unsigned pack_f16(float lo, float hi) {
+    f16x2 v;
+    v[0] = (_Float16)lo;  // nearest, ties to even
+    v[1] = (_Float16)hi;
+    return __builtin_bit_cast(unsigned, v);
+}
+// 16 probabilities as the B operands of the two products with V's 16 tokens
+template <int NV>
+__device__ __forceinline__ void pack_p(const float* p, u32x4 (*f)[NV]) {
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            float lo = p[8 * hf + 2 * w], hi = p[8 * hf + 2 * w + 1];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const unsigned u = pack_f16(lo, hi);
+                f[hf][k][w] = u;
+                const f16x2 r = __builtin_bit_cast(f16x2, u);
+                lo -= float(r[0]);
+                hi -= float(r[1]);
+            }
+        }
+}
+
+template <bool FP8>
+__device__ __forceinline__ u32x4 to_f16(unsigned a, unsigned b) {
+    const u32x2 x = Code<FP8>::dec4_f16(a), y = Code<FP8>::dec4_f16(b);
+    return u32x4{x[0], x[1], y[0], y[1]};
+}
+template <bool FP8>
+__device__ __forceinline__ u32x4 to_bf16(unsigned a, unsigned b) {
+    const u32x2 x = Code<FP8>::dec4_bf16(a), y = Code<FP8>::dec4_bf16(b);
+    return u32x4{x[0], x[1], y[0], y[1]};
+}
+
+
+// The larger of a lane's value and of the lanes 16 and 32 away (the four lanes
+// that share lane % 16), and their sum: register row swaps, no LDS round trip.
+__device__ __forceinline__ float quad_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+}  // namespace
+}  // namespace m3

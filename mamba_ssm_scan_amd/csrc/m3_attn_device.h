@@ -14,6 +14,7 @@ typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
     bf16x2 v;
@@ -123,7 +124,7 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
 
 // 8-bit codes. enc4: four values already divided by the scale, held to the
 // format's range, to the nearest code (ties to even). dec4: four codes as fp32;
-// dec4_bf16: as packed bf16 (both formats are exact there: 8 significant bits).
+// dec4_bf16, dec4_f16: as packed bf16 or fp16 (both formats are exact in both).
 template <bool FP8>
 struct Code;
 template <>
@@ -149,6 +150,11 @@ struct Code<true> {
         const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.f, true);
         return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
     }
+    __device__ __forceinline__ static u32x2 dec4_f16(unsigned w) {
+        const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, false);
+        const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.f, true);
+        return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
+    }
 };
 template <>
 struct Code<false> {
@@ -167,6 +173,14 @@ struct Code<false> {
         float v[4];
         dec4(w, v);
         return u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    }
+    // code + 128 = u as the low byte of the fp16 number 1024 + u, less 1152
+    __device__ __forceinline__ static u32x2 dec4_f16(unsigned w) {
+        const unsigned u = w ^ 0x80808080u;
+        const f16x2 off{_Float16(-1152.f), _Float16(-1152.f)};
+        const f16x2 lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) + off;
+        const f16x2 hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) + off;
+        return u32x2{__builtin_bit_cast(unsigned, lo), __builtin_bit_cast(unsigned, hi)};
     }
 };
 

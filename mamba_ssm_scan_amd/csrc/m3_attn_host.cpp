@@ -157,23 +157,26 @@ m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_hea
 
 namespace m3 {
 
-// Rows of a tile: 16 while a sequence has no more (row, head of a group) pairs,
-// else 32 (each key read once for twice the rows; at headdim above 128 the
-// registers hold 16). Splits: about 4 workgroups a CU, at least 4 tiles of 64
-// keys (one a wave) each.
+// Above 64 (row, head of a group) pairs a sequence, bf16 rows take the kernel that
+// shares each tile of keys among 128 or 256 rows (m3_kv_attend_tile.hip). Else rows
+// of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once
+// for twice the rows; at headdim above 128 the registers hold 16). Splits: about 4
+// workgroups a CU, at least 4 tiles of 64 keys (one a wave) each; 2 a CU, at least 8
+// tiles, for the former.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
-    (void)io;
     (void)causal;
     AttendPlan p{};
     const int64_t group = q_heads / c.heads, pairs = b.max_q * group;
-    p.rows = pairs <= 16 || c.headdim > 128 ? 16 : 32;
+    p.tile = io == M3_BF16 && c.headdim <= 128 && pairs > 64;
+    p.rows = p.tile ? (c.headdim <= 64 ? 128 : 256) : pairs <= 16 || c.headdim > 128 ? 16 : 32;
     p.row_tiles = std::max<int64_t>(1, (pairs + p.rows - 1) / p.rows);
     int64_t tiles = (b.max_kv + 63) / 64;
     if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);
     tiles = std::max<int64_t>(1, tiles);
     const int64_t base = std::max<int64_t>(1, b.batch * c.heads * p.row_tiles);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(1024 / base, (tiles + 3) / 4));
+    const int64_t want = std::max<int64_t>(1, p.tile ? std::min<int64_t>(512 / base, tiles / 8)
+                                                     : std::min<int64_t>(1024 / base, (tiles + 3) / 4));
     p.split_tiles = (tiles + want - 1) / want;
     p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
     if (p.splits > 1) {
@@ -359,7 +362,7 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
             return set_error(M3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, a.plan.total);
         if (!aligned(workspace, 16)) return set_error(M3_EALIGN, "workspace is not 16-byte aligned");
     }
-    if (batch->batch > INT32_MAX / (cache->heads * a.plan.row_tiles * a.plan.splits))
+    if (batch->batch > (INT32_MAX - 7) / (cache->heads * a.plan.row_tiles * a.plan.splits))
         return set_error(M3_EUNSUPPORTED, "too many workgroups");
     const hipError_t e = m3::launch_kv_attend(a);
     if (e != hipSuccess) return set_error(M3_EHIP, "attend launch failed: %s", hipGetErrorString(e));

@@ -50,6 +50,7 @@ hipError_t launch_kv_read(const ReadArgs& a);
 // a group) pairs of one sequence and key head, its keys in tiles of 64, `splits`
 // workgroups along them with `split_tiles` tiles each.
 struct AttendPlan {
+    bool tile;            // the kernel for many rows a sequence
     int32_t rows;         // rows of a tile
     int64_t row_tiles;    // per sequence
     int32_t splits;

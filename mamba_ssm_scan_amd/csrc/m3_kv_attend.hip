@@ -1,11 +1,13 @@
 // m3_kv_attend.hip -- softmax attention over the paged 8-bit cache.
 //
 // o = sum_j p_j v_j with p the softmax of scale * q . k_j, in one pass over the
-// keys with the running maximum m and sum l (log2 domain): when m grows, what
-// was summed is scaled by 2^(m_old - m_new). The codes are exact in bf16, so
-// both products run on bf16 MFMA with the block scales applied to the fp32
-// scores (K) and to the probabilities (V); fp32 rows are split into three bf16
-// parts (24 bits), which keeps every product exact.
+// keys with a running reference and sum (log2 domain): when the reference grows,
+// what was summed is scaled down. The codes are exact in bf16 and fp16, so the
+// products run on MFMA over the codes themselves, q . k in bf16 and p . v in fp16,
+// with the block scales applied in fp32: K's to the scores, V's as log2 vs in the
+// probabilities' exponents (pack_p's comment). fp32 rows are split into three bf16
+// parts (24 bits) and their probabilities into two fp16 parts, so that nothing is
+// rounded to fewer bits.
 //
 // attend_rows_kernel. A workgroup takes up to 16 QT rows of one (sequence, key
 // head) -- a row is a (token, head of the group) pair, so grouped heads share
@@ -22,104 +24,16 @@
 // page numbers are requested before this tile's softmax.
 #include <algorithm>
 
-#include "m3_attn_device.h"
-#include "m3_attn_internal.h"
+#include "m3_attend_common.h"
 
 namespace m3 {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kTile = 64;  // keys of a tile
 constexpr int kWaves = 4;
-
-struct AttendDev {
-    m3_kv_cache c;
-    m3_kv_batch b;
-    m3_rows q;
-    void* out;
-    float* lse;
-    float* part_o;   // [splits][tokens][q_heads][D], sums relative to the part's maximum
-    float* part_ml;  // [splits][tokens][q_heads][2], maximum (log2) and sum
-    int q_heads, group, D, shift, rows;
-    float scale2;    // scale * log2(e)
-    int causal;
-    int64_t window, row_tiles, split_tiles;
-    int splits;
-    bool wide;
-};
-
-__device__ __forceinline__ floatx4 mfma(u32x4 a, u32x4 b, floatx4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                   0, 0);
-}
-
-// Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see.
-struct Span {
-    int64_t lo, hi;
-};
-__device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0) {
-    const int r1 = min(r0 + a.rows, s.n * a.group) - 1;
-    const int64_t base = int64_t(s.held) - s.n;
-    int64_t hi = min(int64_t(s.held), a.b.max_kv), lo = 0;
-    if (a.causal) hi = min(hi, base + r1 / a.group + 1);
-    if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);
-    if (hi <= lo) return Span{0, 0};
-    return Span{lo / kTile, (hi + kTile - 1) / kTile};
-}
-
-// 8 entries of a query row as MFMA operands: one bf16 part, or three that add
-// up to the fp32 value.
-template <typename T>
-struct Parts;
-template <>
-struct Parts<bf16_t> {
-    static constexpr int kN = 1;
-    __device__ __forceinline__ static void load(const bf16_t* p, bool wide, u32x4* f) {
-        if (wide) {
-            f[0] = *reinterpret_cast<const u32x4*>(p);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[0][j] = unsigned(p[2 * j].bits) | unsigned(p[2 * j + 1].bits) << 16;
-        }
-    }
-};
-__device__ __forceinline__ void split3(float lo, float hi, unsigned* w) {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        w[k] = pack_bf16(lo, hi);
-        lo -= __uint_as_float(w[k] << 16);
-        hi -= __uint_as_float(w[k] & 0xffff0000u);
-    }
-}
-template <>
-struct Parts<float> {
-    static constexpr int kN = 3;
-    __device__ __forceinline__ static void load(const float* p, bool wide, u32x4* f) {
-        float v[8];
-        if (wide)
-            load8<true>(p, v);
-        else
-            load8<false>(p, v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            unsigned w[3];
-            split3(v[2 * j], v[2 * j + 1], w);
-#pragma unroll
-            for (int k = 0; k < 3; ++k) f[k][j] = w[k];
-        }
-    }
-};
-
-template <bool FP8>
-__device__ __forceinline__ u32x4 to_bf16(unsigned a, unsigned b) {
-    const u32x2 x = Code<FP8>::dec4_bf16(a), y = Code<FP8>::dec4_bf16(b);
-    return u32x4{x[0], x[1], y[0], y[1]};
-}
 
 template <typename T, bool FP8, int DP, int QT>
 __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
-    constexpr int NP = Parts<T>::kN;   // bf16 parts of a query or probability
+    constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KC = DP / 64;        // 16-code pieces of a key row a lane holds
     constexpr int DT = DP / 16;        // 16-entry tiles of the output
     constexpr int OS = DP + 4;         // LDS row of a wave's output
@@ -222,7 +136,7 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
                 vr[d] = *reinterpret_cast<const u32x4*>(vbase + (vb * D + 16 * d + lr) * 16);
         }
         const float ks = (vb >= 0 ? a.c.k_scale[vb] : 0.f) * a.scale2;
-        const float vs = vb >= 0 ? a.c.v_scale[vb] : 0.f;
+        const VScale vs = v_scale(vb >= 0 ? a.c.v_scale[vb] : 0.f);
         const bool there = vb >= 0;
         const int64_t key0 = tile * kTile + 16 * g;
         const bool masked = tile * kTile < all_lo || tile * kTile + kTile > all_hi || __any(!there);
@@ -260,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
             }
         if (next < t1) load_k(kb2);
 
-        u32x4 pf[QT][2][NP];
+        u32x4 pf[QT][2][NV];
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
             float top = -INFINITY;
@@ -268,57 +182,40 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float v = s[qt][t][e] * ks;
-                    if (masked) {
+                    float v = __builtin_fmaf(s[qt][t][e], ks, vs.log2);
+                    if (masked) {  // (a masked key's scales may be NaN)
                         const int64_t key = key0 + 4 * t + e;
                         v = there && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
                     }
                     s[qt][t][e] = v;
                     top = fmaxf(top, v);
                 }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m2 = fmaxf(mx[qt], top);
+            top = quad_max(top);
+            const float m2 = fmaxf(mx[qt], top - kUp);
             const float mu = m2 == -INFINITY ? 0.f : m2;  // nothing seen yet: 2^-inf = 0 below
             const float fade = __builtin_amdgcn_exp2f(mx[qt] - mu);
             mx[qt] = m2;
             float add = 0.f;
             float p[16];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float w = __builtin_amdgcn_exp2f(s[qt][t][e] - mu);
-                    add += w;
-                    // (a masked key's scale may be NaN)
-                    p[4 * t + e] = masked && s[qt][t][e] == -INFINITY ? 0.f : w * vs;
-                }
-            sum[qt] = sum[qt] * fade + add;
+            for (int j = 0; j < 16; ++j) {
+                p[j] = __builtin_amdgcn_exp2f(s[qt][j / 4][j % 4] - mu);
+                add += p[j];
+            }
+            sum[qt] = sum[qt] * fade + (add == 0.f ? 0.f : add * vs.inv);  // (a block no row sees may hold NaN)
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    if constexpr (NP == 1) {
-                        pf[qt][hf][0][w] = pack_bf16(p[8 * hf + 2 * w], p[8 * hf + 2 * w + 1]);
-                    } else {
-                        unsigned u[3];
-                        split3(p[8 * hf + 2 * w], p[8 * hf + 2 * w + 1], u);
-#pragma unroll
-                        for (int k = 0; k < NP; ++k) pf[qt][hf][k][w] = u[k];
-                    }
-                }
+            pack_p<NV>(p, pf[qt]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const u32x4 vf = to_bf16<FP8>(vr[d][2 * hf], vr[d][2 * hf + 1]);
+                const u32x4 vf = to_f16<FP8>(vr[d][2 * hf], vr[d][2 * hf + 1]);
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) o[qt][d] = mfma(vf, pf[qt][hf][k], o[qt][d]);
+                    for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
             }
         kb = kb2;
         vb = vb2;
@@ -327,8 +224,7 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
     // the four waves' sums, brought to one maximum and added
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
-        sum[qt] += __shfl_xor(sum[qt], 16);
-        sum[qt] += __shfl_xor(sum[qt], 32);
+        sum[qt] = quad_sum(sum[qt]);
         if (g == 0) {
             m_lds[wave][16 * qt + lr] = mx[qt];
             l_lds[wave][16 * qt + lr] = sum[qt];
@@ -443,8 +339,14 @@ hipError_t launch_attend(const AttendArgs& a) {
     AttendDev d{a.c, a.b, a.q, a.out, a.lse, reinterpret_cast<float*>(ws + p.o_off),
                 reinterpret_cast<float*>(ws + p.ml_off), a.q_heads, a.q_heads / a.c.heads, a.c.headdim,
                 __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows, a.scale * kLog2e, a.causal, a.window, p.row_tiles,
-                p.split_tiles, p.splits, a.wide};
-    const int64_t blocks = a.b.batch * a.c.heads * p.row_tiles * p.splits;
+                p.split_tiles, p.splits, a.wide, a.b.batch * a.c.heads * p.row_tiles * p.splits};
+    const int64_t blocks = d.blocks;
+    if (p.tile) {
+        hipError_t e = launch_attend_tile(d, a.stream);
+        if (e != hipSuccess || p.splits == 1) return e;
+        hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned(a.b.tokens * a.q_heads)), dim3(256), 0, a.stream, d);
+        return hipGetLastError();
+    }
     const int qt = p.rows / 16, dp = d.D <= 64 ? 64 : d.D <= 128 ? 128 : 256;
     if (dp == 64) {
         if (qt == 1) launch_rows<T, FP8, 64, 1>(d, blocks, a.stream);
