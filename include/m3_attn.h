@@ -42,7 +42,8 @@ typedef enum m3_kv_format { M3_KV_INT8 = 0, M3_KV_FP8 = 1 } m3_kv_format;
  *   k        [num_pages][heads][page_size / 16][16][headdim]   codes, 8 bits
  *   v        [num_pages][heads][page_size / 16][headdim][16]   codes, 8 bits
  *   k_scale, v_scale [num_pages][heads][page_size / 16]        fp32
- * headdim: a multiple of 16 up to 256. All four are 16-byte aligned. A sequence
+ * headdim: a multiple of 16 up to 256. All four are 16-byte aligned; scales are
+ * not negative. A sequence
  * holds position j in page pages[i][j / page_size]. The 16 slots of a block are
  * written together when its first token comes, so no slot of a block in use is
  * left undefined.

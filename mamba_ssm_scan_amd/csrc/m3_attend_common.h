@@ -24,7 +24,7 @@ struct AttendDev {
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
 };
 
-hipError_t launch_attend_tile(const AttendDev& d, hipStream_t s);
+hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s);
 
 namespace {
 
@@ -123,23 +123,23 @@ __device__ __forceinline__ unsigned pack_f16(float lo, float hi) {
     v[1] = (_Float16)hi;
     return __builtin_bit_cast(unsigned, v);
 }
-// 16 probabilities as the B operands of the two products with V's 16 tokens
+// Two probabilities as word w of the NV parts of a B operand, and 16 of them as the
+// operands of the two products with V's 16 tokens.
+template <int NV>
+__device__ __forceinline__ void pack_pair(float lo, float hi, u32x4 (&f)[NV], int w) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const unsigned u = pack_f16(lo, hi);
+        f[k][w] = u;
+        const f16x2 r = __builtin_bit_cast(f16x2, u);
+        lo -= float(r[0]);
+        hi -= float(r[1]);
+    }
+}
 template <int NV>
 __device__ __forceinline__ void pack_p(const float* p, u32x4 (*f)[NV]) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float lo = p[8 * hf + 2 * w], hi = p[8 * hf + 2 * w + 1];
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const unsigned u = pack_f16(lo, hi);
-                f[hf][k][w] = u;
-                const f16x2 r = __builtin_bit_cast(f16x2, u);
-                lo -= float(r[0]);
-                hi -= float(r[1]);
-            }
-        }
+    for (int j = 0; j < 8; ++j) pack_pair<NV>(p[2 * j], p[2 * j + 1], f[j / 4], j % 4);
 }
 
 template <bool FP8>

@@ -137,7 +137,7 @@ m3_kv_batch bounded(const m3_kv_batch& b, const m3_kv_cache& c) {
     m3_kv_batch r = b;
     r.max_q = b.cu_q ? std::min(b.max_q, b.tokens) : std::min<int64_t>(b.max_q, 1);
     const int64_t room = b.max_pages > (int64_t(1) << 31) / c.page_size ? int64_t(1) << 31 : b.max_pages * c.page_size;
-    r.max_kv = std::min(std::min(b.max_kv, room), int64_t(INT32_MAX));
+    r.max_kv = std::min(std::min(b.max_kv, room), (int64_t(1) << 31) - 256);  // (tile ends stay within 32 bits)
     return r;
 }
 
@@ -157,8 +157,8 @@ m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_hea
 
 namespace m3 {
 
-// Above 64 (row, head of a group) pairs a sequence, bf16 rows take the kernel that
-// shares each tile of keys among 128 or 256 rows (m3_kv_attend_tile.hip). Else rows
+// Above 64 (row, head of a group) pairs a sequence, the kernel that shares each tile
+// of keys among 64 to 256 rows (m3_kv_attend_tile.hip). Else rows
 // of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once
 // for twice the rows; at headdim above 128 the registers hold 16). Splits: about 4
 // workgroups a CU, at least 4 tiles of 64 keys (one a wave) each; 2 a CU, at least 8
@@ -168,8 +168,9 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     (void)causal;
     AttendPlan p{};
     const int64_t group = q_heads / c.heads, pairs = b.max_q * group;
-    p.tile = io == M3_BF16 && c.headdim <= 128 && pairs > 64;
-    p.rows = p.tile ? (c.headdim <= 64 ? 128 : 256) : pairs <= 16 || c.headdim > 128 ? 16 : 32;
+    p.tile = pairs > 64;
+    const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
+    p.rows = p.tile ? (io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width] : pairs <= 16 || width == 2 ? 16 : 32;
     p.row_tiles = std::max<int64_t>(1, (pairs + p.rows - 1) / p.rows);
     int64_t tiles = (b.max_kv + 63) / 64;
     if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);

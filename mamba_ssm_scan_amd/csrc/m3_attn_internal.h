@@ -57,6 +57,8 @@ struct AttendPlan {
     int64_t split_tiles;
     size_t o_off, ml_off, total;  // workspace: parts [splits][tokens][q_heads][D], (max, sum) pairs
 };
+// Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256).
+constexpr int32_t kTileRowsBf16[3] = {128, 256, 128}, kTileRowsF32[3] = {64, 128, 128};
 struct AttendArgs {
     m3_kv_cache c;
     m3_kv_batch b;

@@ -342,7 +342,7 @@ hipError_t launch_attend(const AttendArgs& a) {
                 p.split_tiles, p.splits, a.wide, a.b.batch * a.c.heads * p.row_tiles * p.splits};
     const int64_t blocks = d.blocks;
     if (p.tile) {
-        hipError_t e = launch_attend_tile(d, a.stream);
+        hipError_t e = launch_attend_tile(d, a.io, a.stream);
         if (e != hipSuccess || p.splits == 1) return e;
         hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned(a.b.tokens * a.q_heads)), dim3(256), 0, a.stream, d);
         return hipGetLastError();

@@ -29,7 +29,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
     constexpr int PC = 4 * DP / NT;      // 16-code pieces of K, and of V, a thread brings
     static_assert(PC >= 1 && 4 * DP % NT == 0, "threads and pieces");
     constexpr int KB = 64 * DP * 2;      // bytes of K's, and of V's, image
-    extern __shared__ __align__(16) char lds[];  // [2][K image, V image]
+    extern __shared__ __align__(16) char lds[];  // two K images, two V images
     __shared__ float sc_lds[2][4][4];    // of the tile's blocks: K scale, log2 and inverse of V's, whether held
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -50,14 +50,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
     const int r0 = int(rt) * a.rows;
     const int64_t base = int64_t(sq.held) - sq.n;
     const Span sp = span_of(a, sq, r0);
-    int64_t t0 = sp.lo, t1 = sp.hi;
+    int t0 = int(sp.lo), t1 = int(sp.hi);
     if (a.splits > 1) {
-        t0 = sp.lo + split * a.split_tiles;
-        t1 = min(sp.hi, t0 + a.split_tiles);
+        t0 = int(min(sp.lo + split * a.split_tiles, sp.hi));
+        t1 = int(min(sp.hi, t0 + a.split_tiles));
         if (t0 >= t1) return;
     }
-    const int64_t held = min(int64_t(sq.held), a.b.max_kv);
+    const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
     const int D = a.D;
+    // of a wave's 16 keys and 4 pieces (of 16 codes) of K: this lane's
+    const int key = lane >> 2;
+    auto kc = [&](int j) { return (lane & 3) + (64 * wave + NT * j) % DP / 16; };
 
     // this wave's rows
     u32x4 qf[QT][KM][NP];
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
             for (int k = 0; k < NP; ++k) qf[qt][m][k] = u32x4{0, 0, 0, 0};
             if (live && d < D) Parts<T>::load(p + d, a.wide, qf[qt][m]);
         }
-        khi[qt] = !live ? 0 : int(min(held, a.causal ? base + tok + 1 : held));
+        khi[qt] = !live ? 0 : a.causal ? int(min(int64_t(held), base + tok + 1)) : held;
         klo[qt] = !live || !a.window ? 0 : int(max(base + tok - a.window + 1, int64_t(0)));
         // keys that any and that every live row of the wave sees
         int lo = live ? klo[qt] : 0x7fffffff, hi = khi[qt], alo = klo[qt], ahi = live ? khi[qt] : 0x7fffffff;
@@ -108,156 +111,202 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
         for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
     }
 
-    // what this thread brings of a tile: piece p = tid + NT j of K (16 codes of key
-    // p / (DP / 16)) and of V (16 tokens of entry p % DP), both of block p / DP
+    // what a wave brings of a tile: piece p = 64 wave + lane + NT j of K (16 codes of a
+    // key) and of V (16 tokens of entry p % DP), of block p / DP, so that a wave's
+    // pieces of one j lie in one block and their page is looked up once, in scalars
     const int32_t* pages = a.b.pages + i * a.b.max_pages;
-    const int64_t hoff = int64_t(h) << a.shift;
-    const char* kbase = static_cast<const char*>(a.c.k);
-    const char* vbase = static_cast<const char*>(a.c.v);
+    const int swave = __builtin_amdgcn_readfirstlane(wave);
     u32x4 rk[PC], rv[PC];
     float rks[PC], rvs[PC];
-    int64_t at[PC];
-    auto find = [&](int64_t tile) {
+    bool there[PC];  // whether V's block (and its scales) is held
+    struct Pages {
+        int p[PC];   // page number of this wave's blocks of a tile (-1: none)
+    };
+    auto find = [&](int tile) {
+        Pages r;
 #pragma unroll
         for (int j = 0; j < PC; ++j) {
-            const int64_t blk = tile * 4 + (tid + NT * j) / DP;
-            at[j] = -1;
-            if (tile < t1 && blk * 16 < held) {
-                const int64_t b = block_at(pages, a.b.max_pages, a.c.num_pages, a.shift, H, blk);
-                at[j] = b < 0 ? b : b + hoff;
-            }
+            const int blk = tile * 4 + (64 * swave + NT * j) / DP;
+            r.p[j] = -1;
+            if (tile < t1 && blk < held_blocks && (blk >> a.shift) < a.b.max_pages) r.p[j] = pages[blk >> a.shift];
+        }
+        return r;
+    };
+    auto block = [&](int tile, const Pages& pg, int j) -> int64_t {
+        const int blk = tile * 4 + (64 * swave + NT * j) / DP;
+        const int64_t page = __builtin_amdgcn_readfirstlane(pg.p[j]);
+        if (page < 0 || page >= a.c.num_pages) return -1;
+        return ((page * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
+    };
+    auto fetch_k = [&](int tile, const Pages& pg) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int64_t at = block(tile, pg, j);
+            rk[j] = u32x4{0, 0, 0, 0};
+            if (at >= 0 && 16 * kc(j) < D)
+                rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.k) + at * 16 * D + key * D + 16 * kc(j));
         }
     };
-    auto fetch = [&]() {
+    auto fetch_v = [&](int tile, const Pages& pg) {
 #pragma unroll
         for (int j = 0; j < PC; ++j) {
-            const int p = (tid + NT * j) % DP;
-            const int key = p / (DP / 16), c = p % (DP / 16);
-            rk[j] = rv[j] = u32x4{0, 0, 0, 0};
+            const int64_t at = block(tile, pg, j);
+            const int d = (64 * swave + NT * j) % DP + lane;
+            rv[j] = u32x4{0, 0, 0, 0};
             rks[j] = rvs[j] = 0.f;
-            if (at[j] >= 0) {
-                if (16 * c < D) rk[j] = *reinterpret_cast<const u32x4*>(kbase + (at[j] * 16 + key) * D + 16 * c);
-                if (p < D) rv[j] = *reinterpret_cast<const u32x4*>(vbase + (at[j] * D + p) * 16);
-                rks[j] = a.c.k_scale[at[j]];
-                rvs[j] = a.c.v_scale[at[j]];
+            there[j] = at >= 0;
+            if (at >= 0) {
+                if (d < D) rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.v) + at * 16 * D + d * 16);
+                rks[j] = a.c.k_scale[at];
+                rvs[j] = a.c.v_scale[at];
             }
         }
     };
-    auto stage = [&](int64_t tile, int buf) {
-        char* ki = lds + buf * 2 * KB;
-        char* vi = ki + KB;
+    auto stage_k = [&](int buf) {
 #pragma unroll
         for (int j = 0; j < PC; ++j) {
-            const int p = (tid + NT * j) % DP, blk = (tid + NT * j) / DP;
-            const int key = p / (DP / 16), c = p % (DP / 16);
-            // key 16 blk + 4 t + e is row 4 blk + e of score tile t
-            const int t = key >> 2, r = 4 * blk + (key & 3);
-            const int cg = c / (KM / 2), cj = c % (KM / 2);
-            char* kp = ki + ((t * KM + 2 * cj) * 64 + cg * 16 + r) * 16;
+            const int blk = (64 * swave + NT * j) / DP;
+            // key 16 blk + 4 t + e is row 4 blk + e of score tile t; its place among a
+            // piece's 16 rows is turned by 4 t, so that a wave's writes take all banks
+            const int t = key >> 2, r = (4 * blk + (key & 3) + 4 * t) & 15;
+            const int cg = kc(j) / (KM / 2), cj = kc(j) % (KM / 2);
+            char* kp = lds + buf * KB + ((t * KM + 2 * cj) * 64 + cg * 16 + r) * 16;
             *reinterpret_cast<u32x4*>(kp) = to_bf16<FP8>(rk[j][0], rk[j][1]);
             *reinterpret_cast<u32x4*>(kp + 1024) = to_bf16<FP8>(rk[j][2], rk[j][3]);
+        }
+    };
+    auto stage_v = [&](int tile, int buf) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int p0 = 64 * swave + NT * j;
+            const int blk = p0 / DP, d = p0 % DP + lane;
             u32x4 v = rv[j];
             if (tile * kTile + kTile > held) {  // codes of slots that hold no token may be anything
-                const int nv = int(min(max(held - (tile * kTile + 16 * blk), int64_t(0)), int64_t(16)));
+                const int nv = min(max(held - (tile * kTile + 16 * blk), 0), 16);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int n = min(max(nv - 4 * w, 0), 4);
                     v[w] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
                 }
             }
-            char* vp = vi + ((p / 16) * 2 * 64 + blk * 16 + p % 16) * 16;
+            char* vp = lds + (2 + buf) * KB + ((d / 16) * 2 * 64 + blk * 16 + d % 16) * 16;
             *reinterpret_cast<u32x4*>(vp) = to_f16<FP8>(v[0], v[1]);
             *reinterpret_cast<u32x4*>(vp + 1024) = to_f16<FP8>(v[2], v[3]);
-            if (p == 0) {
+            if (p0 % DP == 0 && lane == 0) {
                 const VScale vs = v_scale(rvs[j]);
                 *reinterpret_cast<floatx4*>(sc_lds[buf][blk]) =
-                    floatx4{rks[j] * a.scale2, vs.log2, vs.inv, at[j] >= 0 ? 1.f : 0.f};
+                    floatx4{rks[j] * a.scale2, vs.log2, vs.inv, there[j] ? 1.f : 0.f};
             }
         }
     };
+    // piece m of score tile t of a K image, and the scores' products with it
+    int kt[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) kt[t] = g * 256 + ((lr + 4 * t) & 15) * 16;
+    floatx4 s[QT][4], sn[QT][4];
+    auto score_step = [&](int buf, int t, int m, floatx4 (&x)[QT][4]) {
+        const u32x4 kf = *reinterpret_cast<const u32x4*>(lds + buf * KB + (t * KM + m) * 1024 + kt[t]);
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            if (m == 0) x[qt][t] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < NP; ++k) x[qt][t] = mfma(kf, qf[qt][m][k], x[qt][t]);
+        }
+    };
+    auto scores = [&](int buf, floatx4 (&x)[QT][4]) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int m = 0; m < KM; ++m) score_step(buf, t, m, x);
+    };
+    auto seen = [&](int tile) { return tile * kTile < w_hi && tile * kTile + kTile > w_lo; };
 
+    // In turn n: the scores of tile n are in registers, V of tile n and K of tile n + 1
+    // in LDS. The products of tile n + 1's scores run beside tile n's exponentials, those
+    // with V beside the conversion of what comes next (K of n + 2, V of n + 1).
+    Pages pgv{}, pgk{};
     if (t0 < t1) {
-        find(t0);
-        fetch();
-        stage(t0, 0);
-        find(t0 + 1);
+        pgk = find(t0);
+        fetch_k(t0, pgk);
+        fetch_v(t0, pgk);
+        pgv = find(t0 + 1);
+        stage_k(0);
+        stage_v(t0, 0);
+        fetch_k(t0 + 1, pgv);
+        pgk = find(t0 + 2);
+        stage_k(1);
+        __syncthreads();
+        if (seen(t0)) scores(0, s);
+        __syncthreads();
     }
-    __syncthreads();
     int buf = 0;
-    for (int64_t tile = t0; tile < t1; ++tile, buf ^= 1) {
-        fetch();  // tile + 1 (nothing after the last)
-        const int64_t k0 = tile * kTile;
-        if (k0 < w_hi && k0 + kTile > w_lo) {
-            const char* ki = lds + buf * 2 * KB + lane * 16;
-            const char* vi = ki + KB;
+    for (int tile = t0; tile < t1; ++tile, buf ^= 1) {
+        fetch_k(tile + 2, pgk);  // (nothing after the last)
+        fetch_v(tile + 1, pgv);
+        pgv = pgk;
+        pgk = find(tile + 3);
+        const int k0 = tile * kTile;
+        if (seen(tile)) {
             const floatx4 sc = *reinterpret_cast<const floatx4*>(sc_lds[buf][g]);
-            const float ks = sc[0], lv = sc[1], iv = sc[2];
-            const bool there = sc[3] != 0.f;
-            // (a scale below 0 would turn the raw maximum round: taken entry by entry)
-            const bool masked = k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f));
-            const int key0 = int(k0) + 16 * g;
-
-            floatx4 s[QT][4];
+            float ks = sc[0], lv = sc[1];
+            const float iv = sc[2];
+            // (a scale below 0 would turn the raw maximum round)
+            if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f || !(ks >= 0.f))) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+                for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                for (int qt = 0; qt < QT; ++qt) s[qt][t] = floatx4{0, 0, 0, 0};
-#pragma unroll
-                for (int m = 0; m < KM; ++m) {
-                    const u32x4 kf = *reinterpret_cast<const u32x4*>(ki + (t * KM + m) * 1024);
-#pragma unroll
-                    for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                        for (int k = 0; k < NP; ++k) s[qt][t] = mfma(kf, qf[qt][m][k], s[qt][t]);
-                }
+                    for (int j = 0; j < 16; ++j) {
+                        const int key = k0 + 16 * g + j;
+                        const float v = __builtin_fmaf(s[qt][j / 4][j % 4], ks, lv);
+                        s[qt][j / 4][j % 4] = sc[3] != 0.f && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
+                    }
+                ks = 1.f;
+                lv = 0.f;
             }
-            u32x4 pf[QT][2][NV];
+            float c[QT];
+            bool up = false;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
-                float top = -INFINITY;
-                if (masked) {
+                float top = s[qt][0][0];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
+                c[qt] = quad_max(__builtin_fmaf(top, ks, lv)) - kUp;
+                up |= c[qt] > mx[qt] + kSlack;
+            }
+            if (__any(up)) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + 4 * t + e;
-                            const float v = __builtin_fmaf(s[qt][t][e], ks, lv);
-                            s[qt][t][e] = there && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
-                            top = fmaxf(top, s[qt][t][e]);
-                        }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) top = fmaxf(top, s[qt][t][e]);
-                    top = __builtin_fmaf(top, ks, lv);
-                }
-                top = quad_max(top) - kUp;
-                if (__any(top > mx[qt] + kSlack)) {
-                    const float m2 = fmaxf(mx[qt], top);
+                for (int qt = 0; qt < QT; ++qt) {
+                    const float m2 = fmaxf(mx[qt], c[qt]);
                     const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
                     mx[qt] = m2;
                     sum[qt] *= fade;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
                 }
-                const float mu = mx[qt] == -INFINITY ? 0.f : mx[qt];
-                float add = 0.f;
-                float p[16];
-                if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = __builtin_amdgcn_exp2f(s[qt][j / 4][j % 4] - mu);
-                } else {
-                    const float c = lv - mu;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c));
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) add += p[j];
-                sum[qt] += add == 0.f ? 0.f : add * iv;  // (a block no row sees may hold NaN)
-                pack_p<NV>(p, pf[qt]);
             }
+            u32x4 pf[QT][2][NV];
+            float p[QT][16];
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) c[qt] = lv - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
+            constexpr int kSteps = 4 * KM;
+#pragma unroll
+            for (int u = 0; u < kSteps; ++u) {
+                score_step(buf ^ 1, u / KM, u % KM, sn);
+#pragma unroll
+                for (int x = u * 16 * QT / kSteps; x < (u + 1) * 16 * QT / kSteps; ++x) {  // its share
+                    const int qt = x / 16, j = x % 16;
+                    p[qt][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c[qt]));
+                }
+            }
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+                float add = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) add += p[qt][j];
+                sum[qt] += add == 0.f ? 0.f : add * iv;  // (a block no row sees may hold NaN)
+                pack_p<NV>(p[qt], pf[qt]);
+            }
+            const char* vi = lds + (2 + buf) * KB + lane * 16;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -268,11 +317,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
 #pragma unroll
                         for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
                 }
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) s[qt][t] = sn[qt][t];
+        } else if (seen(tile + 1)) {
+            scores(buf ^ 1, s);
         }
-        if (tile + 1 < t1) {
-            stage(tile + 1, buf ^ 1);
-            find(tile + 2);
-        }
+        stage_k(buf);
+        stage_v(tile + 1, buf ^ 1);
         __syncthreads();
     }
 
@@ -314,16 +367,22 @@ hipError_t launch_one(const AttendDev& d, hipStream_t s) {
                        kLds, s, d);
     return hipGetLastError();
 }
+// Rows a wave and waves (kTileRowsBf16 and kTileRowsF32 have their products): two tiles of 16 rows a wave
+// where the registers hold them at two waves a SIMD.
 template <typename T, bool FP8>
 hipError_t launch_io(const AttendDev& d, hipStream_t s) {
-    if (d.D <= 64) return launch_one<T, FP8, 64, 2, 4>(d, s);
-    return launch_one<T, FP8, 128, 2, 8>(d, s);
+    constexpr int kQt = sizeof(T) == 2 ? 2 : 1;
+    if (d.D <= 64) return launch_one<T, FP8, 64, kQt, 4>(d, s);
+    if (d.D <= 128) return launch_one<T, FP8, 128, kQt, 8>(d, s);
+    return launch_one<T, FP8, 256, 1, 8>(d, s);
 }
 
 }  // namespace
 
-hipError_t launch_attend_tile(const AttendDev& d, hipStream_t s) {
-    return d.c.format == M3_KV_FP8 ? launch_io<bf16_t, true>(d, s) : launch_io<bf16_t, false>(d, s);
+hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s) {
+    const bool fp8 = d.c.format == M3_KV_FP8;
+    if (io == M3_BF16) return fp8 ? launch_io<bf16_t, true>(d, s) : launch_io<bf16_t, false>(d, s);
+    return fp8 ? launch_io<float, true>(d, s) : launch_io<float, false>(d, s);
 }
 
 }  // namespace m3
