@@ -94,8 +94,9 @@ m3_status check_cache(const m3_kv_cache* c) {
     if (c->heads < 1 || c->heads > 65536) return set_error(M3_EINVAL, "cache heads %d out of range", c->heads);
     if (c->headdim < 16 || c->headdim % 16 != 0 || c->headdim > 256)
         return set_error(M3_EUNSUPPORTED, "cache headdim %d must be a multiple of 16 up to 256", c->headdim);
-    if (c->num_pages * (double)c->heads * c->page_size * c->headdim > 1e15)
-        return set_error(M3_EINVAL, "the cache's sizes are out of range");
+    if (c->num_pages * (double)c->heads * c->page_size * c->headdim > 1e15 ||
+        c->num_pages * (double)c->heads * (c->page_size / M3_KV_BLOCK) >= 2147483648.0)
+        return set_error(M3_EINVAL, "the cache's sizes are out of range");  // (2^31 blocks: 512 GiB of K at headdim 16)
     const void* p[] = {c->k, c->v, c->k_scale, c->v_scale};
     const char* name[] = {"cache k", "cache v", "cache k_scale", "cache v_scale"};
     for (int j = 0; j < 4; ++j) {
@@ -160,9 +161,8 @@ namespace m3 {
 // Above 64 (row, head of a group) pairs a sequence, the kernel that shares each tile
 // of keys among 64 to 256 rows (m3_kv_attend_tile.hip). Else rows
 // of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once
-// for twice the rows; at headdim above 128 the registers hold 16). Splits: about 4
-// workgroups a CU, at least 4 tiles of 64 keys (one a wave) each; 2 a CU, at least 8
-// tiles, for the former.
+// for twice the rows; at headdim above 128 the registers hold 16). Splits: about 2
+// workgroups a CU, at least 4 tiles of 64 keys (one a wave) each, or 8 for the former.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
     (void)causal;
@@ -177,7 +177,7 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     tiles = std::max<int64_t>(1, tiles);
     const int64_t base = std::max<int64_t>(1, b.batch * c.heads * p.row_tiles);
     const int64_t want = std::max<int64_t>(1, p.tile ? std::min<int64_t>(512 / base, tiles / 8)
-                                                     : std::min<int64_t>(1024 / base, (tiles + 3) / 4));
+                                                     : std::min<int64_t>(512 / base, (tiles + 3) / 4));
     p.split_tiles = (tiles + want - 1) / want;
     p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
     if (p.splits > 1) {

@@ -31,8 +31,16 @@ namespace {
 
 constexpr int kWaves = 4;
 
-template <typename T, bool FP8, int DP, int QT>
-__global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
+// Keeps what is computed from a register after this point, where the compiler would
+// convert a tile's codes early and hold them at twice or four times their size.
+__device__ __forceinline__ unsigned here(unsigned w) {
+    asm volatile("" : "+v"(w));
+    return w;
+}
+
+// FULL: headdim is DP, so that every piece is there and loads have constant offsets.
+template <typename T, bool FP8, int DP, int QT, bool FULL>
+__global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * QT > 128) ? 1 : 2) void attend_rows_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KC = DP / 64;        // 16-code pieces of a key row a lane holds
     constexpr int DT = DP / 16;        // 16-entry tiles of the output
@@ -55,17 +63,50 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
     const int r0 = int(rt) * a.rows;
     const int64_t base = int64_t(sq.held) - sq.n;
     const Span sp = span_of(a, sq, r0);
-    int64_t t0 = sp.lo, t1 = sp.hi;
+    int t0 = int(sp.lo), t1 = int(sp.hi);
     if (a.splits > 1) {
-        t0 = sp.lo + split * a.split_tiles;
-        t1 = min(sp.hi, t0 + a.split_tiles);
+        t0 = int(min(sp.lo + split * a.split_tiles, sp.hi));
+        t1 = int(min(sp.hi, t0 + a.split_tiles));
         if (t0 >= t1) return;  // no such part: the join counts the same parts
+    }
+    if (a.c.num_pages == 0) t1 = t0;
+
+    const int D = FULL ? DP : a.D;
+    const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
+    const int32_t* pages = a.b.pages + i * a.b.max_pages;
+    auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
+        if (blk >= held_blocks || (blk >> a.shift) >= a.b.max_pages) return -1;
+        const int64_t p = pages[blk >> a.shift];
+        if (p < 0 || p >= a.c.num_pages) return -1;
+        return ((int(p) * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
+    };
+    // Loads are unconditional (of block 0 where there is none, of piece 0 beyond
+    // headdim): a load behind a branch would wait for those before it. What they bring
+    // is masked below, or meets zeros of q.
+    const char* kbase = static_cast<const char*>(a.c.k) + (lr & 3) * D + (FULL ? 16 * g * KC : 0);
+    const char* vbase = static_cast<const char*>(a.c.v) + lr * 16;
+    u32x4 kr[4][KC];
+    auto load_k = [&](int kb) {
+        const char* p = kbase + uint64_t(unsigned(max(kb, 0))) * unsigned(16 * D);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < KC; ++j) {
+                const int c = g * KC + j;
+                kr[t][j] = *reinterpret_cast<const u32x4*>(p + 4 * t * D + (FULL ? 16 * j : 16 * c < D ? 16 * c : 0));
+            }
+    };
+    int tile = t0 + wave;
+    int kb = -1, vb = -1;
+    if (tile < t1) {
+        kb = find(tile * 4 + (lr >> 2));
+        vb = find(tile * 4 + g);
+        load_k(kb);
     }
 
     // the rows' operands and the keys that each row sees
     u32x4 qf[QT][2 * KC][NP];
-    int64_t klo[QT], khi[QT];
-    const int D = a.D;
+    int klo[QT], khi[QT];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
         const int r = r0 + 16 * qt + lr;
@@ -79,24 +120,13 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
             for (int k = 0; k < NP; ++k) qf[qt][m][k] = u32x4{0, 0, 0, 0};
             if (live && d < D) Parts<T>::load(p + d, a.wide, qf[qt][m]);
         }
-        khi[qt] = !live ? 0 : min(min(int64_t(sq.held), a.b.max_kv), a.causal ? base + tok + 1 : INT64_MAX);
-        klo[qt] = a.window ? base + tok - a.window + 1 : 0;
+        khi[qt] = !live ? 0 : a.causal ? int(min(int64_t(held), base + tok + 1)) : held;
+        klo[qt] = !live || !a.window ? 0 : int(max(base + tok - a.window + 1, int64_t(0)));
     }
     // keys that every row sees: tiles inside need no mask
     const int rl = min(r0 + a.rows, rows) - 1;
-    const int64_t held = min(int64_t(sq.held), a.b.max_kv);
-    const int64_t all_hi = a.causal ? min(held, base + r0 / a.group + 1) : held;
-    const int64_t all_lo = a.window ? base + rl / a.group - a.window + 1 : 0;
-
-    const int32_t* pages = a.b.pages + i * a.b.max_pages;
-    const int64_t hoff = int64_t(h) << a.shift;
-    auto find = [&](int64_t blk) -> int64_t {  // its index for this head, -1: none
-        if (blk * 16 >= held) return -1;
-        const int64_t at = block_at(pages, a.b.max_pages, a.c.num_pages, a.shift, H, blk);
-        return at < 0 ? at : at + hoff;
-    };
-    const char* kbase = static_cast<const char*>(a.c.k);
-    const char* vbase = static_cast<const char*>(a.c.v);
+    const int all_hi = a.causal ? int(max(min(int64_t(held), base + r0 / a.group + 1), int64_t(0))) : held;
+    const int all_lo = a.window ? int(max(base + rl / a.group - a.window + 1, int64_t(0))) : 0;
 
     floatx4 o[QT][DT];
     float mx[QT], sum[QT];
@@ -107,47 +137,54 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
     }
-
-    u32x4 kr[4][KC];
-    auto load_k = [&](int64_t kb) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                const int c = g * KC + j;
-                kr[t][j] = u32x4{0, 0, 0, 0};
-                if (kb >= 0 && 16 * c < D)
-                    kr[t][j] = *reinterpret_cast<const u32x4*>(kbase + (kb * 16 + 4 * t + (lr & 3)) * D + 16 * c);
-            }
-    };
-    int64_t tile = t0 + wave;
-    int64_t kb = -1, vb = -1;
-    if (tile < t1) {
-        kb = find(tile * 4 + (lr >> 2));
-        vb = find(tile * 4 + g);
-        load_k(kb);
-    }
     for (; tile < t1; tile += kWaves) {
         u32x4 vr[DT];
+        {
+            const char* p = vbase + uint64_t(unsigned(max(vb, 0))) * unsigned(16 * D);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            vr[d] = u32x4{0, 0, 0, 0};
-            if (vb >= 0 && 16 * d < D)
-                vr[d] = *reinterpret_cast<const u32x4*>(vbase + (vb * D + 16 * d + lr) * 16);
+            for (int d = 0; d < DT; ++d)
+                vr[d] = *reinterpret_cast<const u32x4*>(p + (FULL || 16 * d < D ? 256 * d : 0));
         }
-        const float ks = (vb >= 0 ? a.c.k_scale[vb] : 0.f) * a.scale2;
-        const VScale vs = v_scale(vb >= 0 ? a.c.v_scale[vb] : 0.f);
         const bool there = vb >= 0;
-        const int64_t key0 = tile * kTile + 16 * g;
-        const bool masked = tile * kTile < all_lo || tile * kTile + kTile > all_hi || __any(!there);
-        const int64_t next = tile + kWaves;
-        int64_t kb2 = -1, vb2 = -1;
+        float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
+        VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
+        const int k0 = tile * kTile, next = tile + kWaves;
+        int kb2 = -1, vb2 = -1;
         if (next < t1) {
             kb2 = find(next * 4 + (lr >> 2));
             vb2 = find(next * 4 + g);
         }
-        if (masked) {  // codes of slots that hold no token may be anything
-            const int nv = int(min(max(held - key0, int64_t(0)), int64_t(16)));
+
+        floatx4 s[QT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int m = 0; m < 2 * KC; ++m) {
+                const u32x4 kf = to_bf16<FP8>(here(kr[t][m / 2][2 * (m & 1)]), here(kr[t][m / 2][2 * (m & 1) + 1]));
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) {
+                    if (m == 0) s[qt][t] = floatx4{0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) s[qt][t] = mfma(kf, qf[qt][m][k], s[qt][t]);
+                }
+                if (m % 4 == 3 || m == 2 * KC - 1) __builtin_amdgcn_sched_barrier(0);  // (conversions one after the other)
+            }
+        if (next < t1) load_k(kb2);
+
+        // (a scale below 0 would turn the raw maximum round)
+        if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f))) {
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int key = k0 + 16 * g + j;
+                    const float v = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
+                    s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
+                }
+            ks = 1.f;
+            vs.log2 = 0.f;
+            // codes of slots that hold no token may be anything
+            const int nv = there ? min(max(held - (k0 + 16 * g), 0), 16) : 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int n = min(max(nv - 4 * w, 0), 4);
@@ -156,66 +193,51 @@ __global__ __launch_bounds__(64 * kWaves) void attend_rows_kernel(AttendDev a) {
                 for (int d = 0; d < DT; ++d) vr[d][w] &= keep;
             }
         }
-
-        floatx4 s[QT][4];
+        float c[QT];
+        bool up = false;
 #pragma unroll
-        for (int qt = 0; qt < QT; ++qt)
+        for (int qt = 0; qt < QT; ++qt) {
+            float top = s[qt][0][0];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) s[qt][t] = floatx4{0, 0, 0, 0};
+            for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
+            c[qt] = quad_max(__builtin_fmaf(top, ks, vs.log2)) - kUp;
+            up |= c[qt] > mx[qt] + kSlack;
+        }
+        if (__any(up)) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int qt = 0; qt < QT; ++qt) {
+                const float m2 = fmaxf(mx[qt], c[qt]);
+                const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
+                mx[qt] = m2;
+                sum[qt] *= fade;
 #pragma unroll
-            for (int m = 0; m < 2 * KC; ++m) {
-                const u32x4 kf = to_bf16<FP8>(kr[t][m / 2][2 * (m & 1)], kr[t][m / 2][2 * (m & 1) + 1]);
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) s[qt][t] = mfma(kf, qf[qt][m][k], s[qt][t]);
+                for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
             }
-        if (next < t1) load_k(kb2);
-
+        }
         u32x4 pf[QT][2][NV];
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = __builtin_fmaf(s[qt][t][e], ks, vs.log2);
-                    if (masked) {  // (a masked key's scales may be NaN)
-                        const int64_t key = key0 + 4 * t + e;
-                        v = there && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
-                    }
-                    s[qt][t][e] = v;
-                    top = fmaxf(top, v);
-                }
-            top = quad_max(top);
-            const float m2 = fmaxf(mx[qt], top - kUp);
-            const float mu = m2 == -INFINITY ? 0.f : m2;  // nothing seen yet: 2^-inf = 0 below
-            const float fade = __builtin_amdgcn_exp2f(mx[qt] - mu);
-            mx[qt] = m2;
+            const float off = vs.log2 - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
             float add = 0.f;
             float p[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(s[qt][j / 4][j % 4] - mu);
+                p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, off));
                 add += p[j];
             }
-            sum[qt] = sum[qt] * fade + (add == 0.f ? 0.f : add * vs.inv);  // (a block no row sees may hold NaN)
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
+            sum[qt] += add == 0.f ? 0.f : add * vs.inv;  // (a block no row sees may hold NaN)
             pack_p<NV>(p, pf[qt]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                const u32x4 vf = to_f16<FP8>(vr[d][2 * hf], vr[d][2 * hf + 1]);
+                const u32x4 vf = to_f16<FP8>(here(vr[d][2 * hf]), here(vr[d][2 * hf + 1]));
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                     for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
+                if (hf && d % 2) __builtin_amdgcn_sched_barrier(0);
             }
         kb = kb2;
         vb = vb2;
@@ -329,8 +351,12 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a) {
 }
 
 template <typename T, bool FP8, int DP, int QT>
-void launch_rows(const AttendDev& d, int64_t blocks, hipStream_t s) {
-    hipLaunchKernelGGL((attend_rows_kernel<T, FP8, DP, QT>), dim3(unsigned(blocks)), dim3(64 * kWaves), 0, s, d);
+void launch_rows(const AttendDev& d, hipStream_t s) {
+    const dim3 grid(unsigned(d.blocks)), block(64 * kWaves);
+    if (d.D == DP)
+        hipLaunchKernelGGL((attend_rows_kernel<T, FP8, DP, QT, true>), grid, block, 0, s, d);
+    else
+        hipLaunchKernelGGL((attend_rows_kernel<T, FP8, DP, QT, false>), grid, block, 0, s, d);
 }
 template <typename T, bool FP8>
 hipError_t launch_attend(const AttendArgs& a) {
@@ -340,7 +366,6 @@ hipError_t launch_attend(const AttendArgs& a) {
                 reinterpret_cast<float*>(ws + p.ml_off), a.q_heads, a.q_heads / a.c.heads, a.c.headdim,
                 __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows, a.scale * kLog2e, a.causal, a.window, p.row_tiles,
                 p.split_tiles, p.splits, a.wide, a.b.batch * a.c.heads * p.row_tiles * p.splits};
-    const int64_t blocks = d.blocks;
     if (p.tile) {
         hipError_t e = launch_attend_tile(d, a.io, a.stream);
         if (e != hipSuccess || p.splits == 1) return e;
@@ -349,13 +374,13 @@ hipError_t launch_attend(const AttendArgs& a) {
     }
     const int qt = p.rows / 16, dp = d.D <= 64 ? 64 : d.D <= 128 ? 128 : 256;
     if (dp == 64) {
-        if (qt == 1) launch_rows<T, FP8, 64, 1>(d, blocks, a.stream);
-        else launch_rows<T, FP8, 64, 2>(d, blocks, a.stream);
+        if (qt == 1) launch_rows<T, FP8, 64, 1>(d, a.stream);
+        else launch_rows<T, FP8, 64, 2>(d, a.stream);
     } else if (dp == 128) {
-        if (qt == 1) launch_rows<T, FP8, 128, 1>(d, blocks, a.stream);
-        else launch_rows<T, FP8, 128, 2>(d, blocks, a.stream);
+        if (qt == 1) launch_rows<T, FP8, 128, 1>(d, a.stream);
+        else launch_rows<T, FP8, 128, 2>(d, a.stream);
     } else {
-        launch_rows<T, FP8, 256, 1>(d, blocks, a.stream);
+        launch_rows<T, FP8, 256, 1>(d, a.stream);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
