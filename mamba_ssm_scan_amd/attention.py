@@ -13,8 +13,8 @@ A prompt, or a ragged batch, gives its row offsets `cu_q` and the longest `max_q
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -71,18 +71,7 @@ def _lib():
     return _ready
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """The device and stream of a call: its allocations belong to that stream, so their memory is not handed on early."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
-
-
-def _same(t: torch.Tensor, name: str, device, dtype, shape=None):
+def _complain(t, name: str, device, dtype, shape):
     if not isinstance(t, torch.Tensor) or t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
@@ -91,20 +80,27 @@ def _same(t: torch.Tensor, name: str, device, dtype, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _dense(t: torch.Tensor, name: str, device, dtype, shape=None):
-    _same(t, name, device, dtype, shape)
+def _dense(t: torch.Tensor, name: str, device, dtype, shape=None) -> int:
+    """The address of a contiguous tensor of this device, type and shape."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or (shape is not None
+                                                                                         and t.shape != shape):
+        _complain(t, name, device, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, device, dtype, shape=None) -> M3Rows:
     """[tokens][heads][dim] rows where they lie: the entries of a head contiguous, any other strides."""
-    _same(t, name, device, dtype, shape)
-    if t.dim() != 3:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or (shape is not None
+                                                                                         and t.shape != shape):
+        _complain(t, name, device, dtype, shape)
+    st = t.stride()
+    if len(st) != 3:
         raise ValueError(f"{name} must be [tokens][heads][dim]")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if st[2] != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}: the entries of a head must be contiguous")
-    return M3Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return M3Rows(t.data_ptr(), st[0], st[1])
 
 
 def _device_of(t: torch.Tensor, name: str):
@@ -113,11 +109,37 @@ def _device_of(t: torch.Tensor, name: str):
     return t.device
 
 
+def _on_stream(fn):
+    """Runs a call on its device and stream: its allocations then belong to that stream, so that their memory is not
+    handed on early. fn(..., stream=the raw handle)."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        dev = getattr(first, "device", None)
+        if stream is None:
+            if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(dev):
+                return fn(first, *args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+# the current stream's raw handle, without the Stream object around it where torch has that call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _rotary(inv_freq, device, interleaved, mscale) -> M3Rotary:
-    _dense(inv_freq, "inv_freq", device, torch.float32)
+    p = _dense(inv_freq, "inv_freq", device, torch.float32)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot / 2]")
-    return M3Rotary(inv_freq.data_ptr(), 2 * inv_freq.numel(), int(bool(interleaved)), float(mscale))
+    return M3Rotary(p, 2 * inv_freq.numel(), int(bool(interleaved)), float(mscale))
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[str] = None, factor: float = 1.0,
@@ -153,24 +175,23 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[str] 
     return f.to(torch.float32).to(device), mscale
 
 
-def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None,
-         stream=None):
+@_on_stream
+def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None):
     """m3_rope: x [tokens][heads][dim] (bf16 or fp32) turned by positions [tokens] int32; returns out.
 
-    backward: the transposed map (dL/dx from x = dL/dy). out may be x itself.
+    backward: the transposed map (dL/dx from x = dL/dy). out may be x itself. stream: the current one unless given.
     """
-    dev = _device_of(x, "x")
-    code = binding._io_code(x.dtype)
-    rx = _rows(x, "x", dev, x.dtype)
-    T, H, D = x.shape
-    _dense(positions, "positions", dev, torch.int32, (T,))
+    dev, dt = _device_of(x, "x"), x.dtype
+    code = binding._io_code(dt)
+    rx = _rows(x, "x", dev, dt)
+    shape = x.shape
+    T, H, D = shape
+    pos = _dense(positions, "positions", dev, torch.int32, (T,))
     rot = _rotary(inv_freq, dev, interleaved, mscale)
-    lib = _lib()
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
-        ry = _rows(out, "out", dev, x.dtype, (T, H, D))
-        check(lib.m3_rope(rx, ry, T, H, D, code, positions.data_ptr(), rot, int(bool(backward)), s))
+    if out is None:
+        out = x.new_empty(shape)
+    ry = _rows(out, "out", dev, dt, shape)
+    check(_lib().m3_rope(rx, ry, T, H, D, code, pos, rot, 1 if backward else 0, _handle(dev)))
     return out
 
 
@@ -199,6 +220,7 @@ class KVCache:
         self.device, self.heads, self.head_dim, self.page_size = dev, H, D, S * BLOCK
         self._c = M3KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, S * BLOCK, H, D,
                             FORMATS[k.dtype])
+        self._sizes = {}  # workspace bytes by a call's sizes
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, heads: int, head_dim: int, dtype=torch.int8, device="cuda"):
@@ -213,88 +235,96 @@ class KVCache:
 
     def _batch(self, tokens, kv_len, pages, cu_q, max_q, max_kv) -> M3KvBatch:
         dev = self.device
-        _dense(kv_len, "kv_len", dev, torch.int32)
-        _dense(pages, "pages", dev, torch.int32)
+        lens, table = _dense(kv_len, "kv_len", dev, torch.int32), _dense(pages, "pages", dev, torch.int32)
         if kv_len.dim() != 1 or pages.dim() != 2 or pages.shape[0] != kv_len.shape[0]:
             raise ValueError("kv_len must be [batch] and pages [batch][max_pages]")
-        b = kv_len.shape[0]
+        b, room = pages.shape
+        cu = None
         if cu_q is not None:
-            _dense(cu_q, "cu_q", dev, torch.int32, (b + 1,))
+            cu = _dense(cu_q, "cu_q", dev, torch.int32, (b + 1,))
         elif tokens != b:
             raise ValueError(f"{tokens} rows for {b} sequences need cu_q")
-        cap = pages.shape[1] * self.page_size
-        return M3KvBatch(b, tokens, pages.shape[1], int(max_q), cap if max_kv is None else int(max_kv),
-                         None if cu_q is None else cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr())
+        return M3KvBatch(b, tokens, room, max_q, room * self.page_size if max_kv is None else max_kv, cu, lens, table)
 
+    @_on_stream
     def append(self, k, v, kv_len, pages, *, cu_q=None, max_q: int = 1, q=None, q_out=None, inv_freq=None,
-               interleaved: bool = False, mscale: float = 1.0, stream=None):
+               interleaved: bool = False, mscale: float = 1.0):
         """m3_kv_append: k, v [tokens][heads][dim] (bf16 or fp32) into the cache, the keys turned by inv_freq (None:
-        as they are). With q [tokens][q_heads][dim], returns it turned by the same positions."""
-        dev, T = self.device, k.shape[0]
-        code = binding._io_code(k.dtype)
+        as they are). With q [tokens][q_heads][dim], returns it turned by the same positions. stream: the current one
+        unless given."""
+        dev, dt, T = self.device, k.dtype, k.shape[0]
+        code = binding._io_code(dt)
         shape = (T, self.heads, self.head_dim)
-        rk, rv = _rows(k, "k", dev, k.dtype, shape), _rows(v, "v", dev, k.dtype, shape)
+        rk, rv = _rows(k, "k", dev, dt, shape), _rows(v, "v", dev, dt, shape)
         b = self._batch(T, kv_len, pages, cu_q, max_q, None)
         rot = None if inv_freq is None else _rotary(inv_freq, dev, interleaved, mscale)
-        lib = _lib()
-        with _on(dev, stream) as s:
-            rq = ro = None
-            qh = 0
-            if q is not None:
-                rq, qh = _rows(q, "q", dev, k.dtype), q.shape[1]
-                if q_out is None:
-                    q_out = torch.empty((T, qh, self.head_dim), dtype=k.dtype, device=dev)
-                _same(q, "q", dev, k.dtype, (T, qh, self.head_dim))
-                ro = _rows(q_out, "q_out", dev, k.dtype, (T, qh, self.head_dim))
-            elif q_out is not None:
-                raise ValueError("q_out without q")
-            check(lib.m3_kv_append(self._c, b, rk, rv, rq, ro, qh, code, rot, s))
+        rq = ro = None
+        qh = 0
+        if q is not None:
+            rq = _rows(q, "q", dev, dt)
+            shape = q.shape
+            qh = shape[1]
+            if shape[0] != T or shape[2] != self.head_dim:
+                raise ValueError(f"q has shape {tuple(shape)}, expected ({T}, q_heads, {self.head_dim})")
+            if q_out is None:
+                q_out = q.new_empty(shape)
+            ro = _rows(q_out, "q_out", dev, dt, shape)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        check(_lib().m3_kv_append(self._c, b, rk, rv, rq, ro, qh, code, rot, _handle(dev)))
         return q_out
 
-    def read(self, first, count, pages, max_count: int, dtype=torch.bfloat16, stream=None):
+    @_on_stream
+    def read(self, first, count, pages, max_count: int, dtype=torch.bfloat16):
         """m3_kv_read: the values held at positions first[i] .. first[i] + count[i] - 1 of each sequence, as k, v
-        [batch][max_count][heads][dim]; rows past count are zero."""
+        [batch][max_count][heads][dim]; rows past count are zero. stream: the current one unless given."""
         dev = self.device
         code = binding._io_code(dtype)
-        _dense(first, "first", dev, torch.int32)
+        at = _dense(first, "first", dev, torch.int32)
         b = first.numel()
-        _dense(count, "count", dev, torch.int32, (b,))
-        _dense(pages, "pages", dev, torch.int32)
+        n, table = _dense(count, "count", dev, torch.int32, (b,)), _dense(pages, "pages", dev, torch.int32)
         if first.dim() != 1 or pages.dim() != 2 or pages.shape[0] != b:
             raise ValueError("first and count must be [batch] and pages [batch][max_pages]")
         if max_count < 0:
             raise ValueError(f"max_count {max_count} < 0")
-        lib = _lib()
-        with _on(dev, stream) as s:
-            k, v = (torch.empty((b, max_count, self.heads, self.head_dim), dtype=dtype, device=dev) for _ in range(2))
-            check(lib.m3_kv_read(self._c, b, first.data_ptr(), count.data_ptr(), pages.data_ptr(), pages.shape[1],
-                                 int(max_count), k.data_ptr(), v.data_ptr(), code, s))
+        shape = (b, max_count, self.heads, self.head_dim)
+        k, v = first.new_empty(shape, dtype=dtype), first.new_empty(shape, dtype=dtype)
+        check(_lib().m3_kv_read(self._c, b, at, n, table, pages.shape[1], max_count, k.data_ptr(), v.data_ptr(), code,
+                                _handle(dev)))
         return k, v
 
+    @_on_stream
     def attend(self, q, kv_len, pages, *, cu_q=None, max_q: int = 1, max_kv: Optional[int] = None,
-               scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None, lse=False, stream=None):
+               scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None, lse=False):
         """m3_kv_attend: q [tokens][q_heads][dim] over the cache; returns out, or (out, lse) with lse=True.
 
         scale: 1 / sqrt(dim) unless given. causal: a row sees the keys up to its own position; window > 0: only the
         last `window` of them. A row that sees nothing gives 0 (and lse -inf). max_kv: at least the largest kv_len,
-        the page table's room unless given (a tighter bound saves empty workgroups).
+        the page table's room unless given. stream: the current one unless given.
         """
-        dev = self.device
-        code = binding._io_code(q.dtype)
-        rq = _rows(q, "q", dev, q.dtype)
-        T, H, D = q.shape
+        dev, dt = self.device, q.dtype
+        code = binding._io_code(dt)
+        rq = _rows(q, "q", dev, dt)
+        shape = q.shape
+        T, H, D = shape
         if D != self.head_dim:
             raise ValueError(f"q has heads of {D} entries, the cache of {self.head_dim}")
         b = self._batch(T, kv_len, pages, cu_q, max_q, max_kv)
-        sc = 1.0 / math.sqrt(D) if scale is None else float(scale)
+        if scale is None:
+            scale = 1.0 / math.sqrt(D)
         lib = _lib()
-        with _on(dev, stream) as s:
-            if out is None:
-                out = torch.empty((T, H, D), dtype=q.dtype, device=dev)
-            _dense(out, "out", dev, q.dtype, (T, H, D))
-            l = torch.empty((T, H), dtype=torch.float32, device=dev) if lse else None
-            n = lib.m3_kv_attend_workspace_size(self._c, b, H, code, int(bool(causal)), int(window))
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-            check(lib.m3_kv_attend(self._c, b, rq, out.data_ptr(), l.data_ptr() if lse else None, H, code, sc,
-                                   int(bool(causal)), int(window), ws.data_ptr() if n else None, n, s))
-        return (out, l) if lse else out
+        if out is None:
+            out = q.new_empty(shape)
+        o = _dense(out, "out", dev, dt, shape)
+        z = q.new_empty((T, H), dtype=torch.float32) if lse else None
+        causal = 1 if causal else 0
+        key = (b.batch, T, b.max_pages, b.max_q, b.max_kv, cu_q is None, H, code, causal, window)
+        n = self._sizes.get(key)
+        if n is None:
+            if len(self._sizes) > 4096:
+                self._sizes.clear()
+            n = self._sizes[key] = lib.m3_kv_attend_workspace_size(self._c, b, H, code, causal, window)
+        ws = q.new_empty(n, dtype=torch.uint8) if n else None
+        check(lib.m3_kv_attend(self._c, b, rq, o, z.data_ptr() if lse else None, H, code, scale, causal, window,
+                               ws.data_ptr() if n else None, n, _handle(dev)))
+        return (out, z) if lse else out

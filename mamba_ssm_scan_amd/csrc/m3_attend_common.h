@@ -13,8 +13,13 @@ struct AttendDev {
     m3_rows q;
     void* out;
     float* lse;
-    float* part_o;   // [splits][tokens][q_heads][D], sums in the part's unit
-    float* part_ml;  // [splits][tokens][q_heads][2], log2 of the part's unit and its sum
+    // Parts of rows whose keys several workgroups share: the sums [..][D] in the part's
+    // unit, and (log2 of the unit, the probabilities' sum) [..][2]. By [split][token]
+    // [head], or with even shares by [slot][row of the tile] (m3_kv_attend.hip).
+    float* part_o;
+    float* part_ml;
+    int* shares;     // even shares: tiles of a share, then the items' first tiles [items + 1]
+    int items;       // (sequence, row tile) pairs; 0: no even shares
     int q_heads, group, D, shift, rows;
     float scale2;    // scale * log2(e)
     int causal;

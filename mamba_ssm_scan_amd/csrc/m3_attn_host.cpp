@@ -159,10 +159,14 @@ m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_hea
 namespace m3 {
 
 // Above 64 (row, head of a group) pairs a sequence, the kernel that shares each tile
-// of keys among 64 to 256 rows (m3_kv_attend_tile.hip). Else rows
-// of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once
-// for twice the rows; at headdim above 128 the registers hold 16). Splits: about 2
-// workgroups a CU, at least 4 tiles of 64 keys (one a wave) each, or 8 for the former.
+// of keys among 64 to 256 rows (m3_kv_attend_tile.hip); its keys are split, at least 8
+// tiles of 64 a workgroup, while there are fewer row tiles than two a CU. Else rows of
+// a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
+// twice the rows; at headdim above 128 the registers hold 16). A row tile and key head
+// is a workgroup's where that makes two workgroups a CU (128 sequences of 2112 tokens, 4
+// heads: 56 us, 66 by even shares and their join; of 127 .. 4095 tokens: 73 and 77) or
+// every sequence is short (8 tiles: two a wave); else all tiles are dealt out in even
+// shares, which a loose max_kv does not hurt.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
     (void)causal;
@@ -175,17 +179,25 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     int64_t tiles = (b.max_kv + 63) / 64;
     if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);
     tiles = std::max<int64_t>(1, tiles);
-    const int64_t base = std::max<int64_t>(1, b.batch * c.heads * p.row_tiles);
-    const int64_t want = std::max<int64_t>(1, p.tile ? std::min<int64_t>(512 / base, tiles / 8)
-                                                     : std::min<int64_t>(512 / base, (tiles + 3) / 4));
-    p.split_tiles = (tiles + want - 1) / want;
-    p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
-    if (p.splits > 1) {
-        const size_t rows = size_t(p.splits) * size_t(b.tokens) * size_t(q_heads);
-        p.o_off = 0;
-        p.ml_off = rows * size_t(c.headdim) * 4;
-        p.total = p.ml_off + rows * 8;
+    const int64_t items = b.batch * p.row_tiles, base = std::max<int64_t>(1, items * c.heads);
+    p.splits = 1;
+    p.split_tiles = tiles;
+    p.blocks = base;
+    size_t parts = 0;  // rows of parts
+    if (p.tile) {
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / base, tiles / 8));
+        p.split_tiles = (tiles + want - 1) / want;
+        p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
+        p.blocks = base * p.splits;
+        if (p.splits > 1) parts = size_t(p.splits) * size_t(b.tokens) * size_t(q_heads);
+    } else if (tiles > 8 && base < 512 && items <= kAttendItems && items * tiles <= INT32_MAX) {
+        p.items = int32_t(items);
+        p.blocks = std::min<int64_t>(512, (base * tiles + 3) / 4);
+        parts = size_t(2 * p.blocks) * size_t(p.rows);
+        p.o_off = (size_t(items + 2) * 4 + 255) / 256 * 256;
     }
+    p.ml_off = p.o_off + parts * size_t(c.headdim) * 4;
+    p.total = parts ? p.ml_off + parts * 8 : 0;
     return p;
 }
 
@@ -363,8 +375,7 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
             return set_error(M3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, a.plan.total);
         if (!aligned(workspace, 16)) return set_error(M3_EALIGN, "workspace is not 16-byte aligned");
     }
-    if (batch->batch > (INT32_MAX - 7) / (cache->heads * a.plan.row_tiles * a.plan.splits))
-        return set_error(M3_EUNSUPPORTED, "too many workgroups");
+    if (a.plan.blocks > INT32_MAX - 7) return set_error(M3_EUNSUPPORTED, "too many workgroups");
     const hipError_t e = m3::launch_kv_attend(a);
     if (e != hipSuccess) return set_error(M3_EHIP, "attend launch failed: %s", hipGetErrorString(e));
     return M3_OK;

@@ -47,16 +47,21 @@ struct ReadArgs {
 hipError_t launch_kv_read(const ReadArgs& a);
 
 // How the rows and keys of an attend call are cut: a tile of `rows` (row, head of
-// a group) pairs of one sequence and key head, its keys in tiles of 64, `splits`
-// workgroups along them with `split_tiles` tiles each.
+// a group) pairs of one sequence and key head, its keys in tiles of 64. The kernel
+// for many rows: `splits` workgroups along a row tile's keys, `split_tiles` tiles
+// each. The kernel for few: `items` > 0 gives every workgroup an even share of all
+// tiles, 0 a row tile each.
 struct AttendPlan {
     bool tile;            // the kernel for many rows a sequence
     int32_t rows;         // rows of a tile
     int64_t row_tiles;    // per sequence
     int32_t splits;
     int64_t split_tiles;
-    size_t o_off, ml_off, total;  // workspace: parts [splits][tokens][q_heads][D], (max, sum) pairs
+    int32_t items;        // (sequence, row tile) pairs
+    int64_t blocks;       // workgroups
+    size_t o_off, ml_off, total;  // workspace: the shares (even ones), sums of parts, (unit, sum) pairs
 };
+constexpr int32_t kAttendItems = 2048;  // most items whose first tiles a workgroup holds
 // Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256).
 constexpr int32_t kTileRowsBf16[3] = {128, 256, 128}, kTileRowsF32[3] = {64, 128, 128};
 struct AttendArgs {

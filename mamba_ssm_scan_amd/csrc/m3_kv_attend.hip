@@ -30,12 +30,79 @@ namespace m3 {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kMaxItems = kAttendItems;
 
 // Keeps what is computed from a register after this point, where the compiler would
 // convert a tile's codes early and hold them at twice or four times their size.
 __device__ __forceinline__ unsigned here(unsigned w) {
     asm volatile("" : "+v"(w));
     return w;
+}
+
+// Even shares. The tiles of all (sequence, row tile) items lie one after the other,
+// an item's once for each key head; a workgroup takes the same number of them,
+// whatever the lengths, and a row tile's keys that several share are joined
+// afterwards. An item's keys for one head are one run: the share that holds its
+// first tile but not its last writes part 0 to its slot 2 w + 1, a later share w
+// the next part to slot 2 w. Every workgroup forms the items' first tiles itself
+// (one scan of the lengths), the first also stores them for the join. Returns the
+// tiles of a share: a multiple of 4, one tile a wave at least.
+__device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* scan) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (a.items + 64 * kWaves - 1) / (64 * kWaves);
+    const int e0 = threadIdx.x * per, e1 = min(e0 + per, a.items);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        const Seq sq = seq_of(a.b, e / int(a.row_tiles));
+        const int r0 = e % int(a.row_tiles) * a.rows;
+        const Span sp = r0 < sq.n * a.group ? span_of(a, sq, r0) : Span{0, 0};
+        first[e] = int(sp.hi - sp.lo);
+        sum += int(sp.hi - sp.lo);
+    }
+    int up = sum;  // over the wave, then over the waves before
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const int o = __shfl_up(up, k);
+        up += lane >= k ? o : 0;
+    }
+    if (lane == 63) scan[wave] = up;
+    __syncthreads();
+    int at = up - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        at += w < wave ? scan[w] : 0;
+        total += scan[w];
+    }
+    for (int e = e0; e < e1; ++e) {
+        const int n = first[e];
+        first[e] = at;
+        at += n;
+    }
+    if (threadIdx.x == 0) first[a.items] = total;
+    __syncthreads();
+    const int64_t all = int64_t(total) * a.c.heads;
+    const int share = int((all + 4 * a.blocks - 1) / (4 * a.blocks)) * 4;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) a.shares[0] = max(share, 4);
+        for (int e = threadIdx.x; e <= a.items; e += 64 * kWaves) a.shares[1 + e] = first[e];
+    }
+    return max(share, 4);
+}
+// Rows of items that see no key belong to no share: every workgroup clears its part.
+template <typename T>
+__device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) {
+    for (int e = blockIdx.x; e < a.items; e += int(a.blocks)) {
+        if (first[e + 1] != first[e]) continue;
+        const Seq sq = seq_of(a.b, e / int(a.row_tiles));
+        const int r0 = e % int(a.row_tiles) * a.rows, r1 = min(r0 + a.rows, sq.n * a.group);
+        const int D = a.D, H = a.c.heads;
+        for (int64_t k = threadIdx.x; k < int64_t(r1 - r0) * H * D; k += 64 * kWaves) {
+            const int d = int(k % D), h = int(k / D % H), r = r0 + int(k / D / H);
+            const int64_t at = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+            Io<T>::store(static_cast<T*>(a.out), at * D + d, 0.f);
+            if (a.lse && d == 0) a.lse[at] = -INFINITY;
+        }
+    }
 }
 
 // FULL: headdim is DP, so that every piece is there and loads have constant offsets.
@@ -50,24 +117,58 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, g = lane >> 4;
-    int64_t id = blockIdx.x;
-    const int split = int(id % a.splits);
-    id /= a.splits;
-    const int64_t rt = id % a.row_tiles;
-    id /= a.row_tiles;
-    const int H = a.c.heads, h = int(id % H);
-    const int64_t i = id / H;
+    const int H = a.c.heads;
+    __shared__ int first_lds[kMaxItems + 1];
+    __shared__ int scan_lds[kWaves];
+    int share = 0, w = blockIdx.x;  // tiles of a share; this one
+    int64_t x = 0, xe = 1;          // what is left of it
+    if (a.items) {
+        share = even_shares(a, first_lds, scan_lds);
+        x = int64_t(w) * share;
+        xe = min(x + share, int64_t(H) * first_lds[a.items]);
+        zero_rows<T>(a, first_lds);
+    }
+    while (x < xe) {  // (a share may end one row tile's keys and begin the next's)
+    int64_t i, rt;
+    int h, t0, t1;
+    bool whole = true;
+    if (a.items) {
+        int e = 0;
+        for (int hi = a.items - 1; e < hi;) {  // the last item that begins at or before x
+            const int mid = (e + hi + 1) / 2;
+            if (int64_t(H) * first_lds[mid] <= x) e = mid;
+            else hi = mid - 1;
+        }
+        const int n = first_lds[e + 1] - first_lds[e];
+        const int64_t off = x - int64_t(H) * first_lds[e];
+        h = int(off / n);
+        t0 = int(off - int64_t(h) * n);
+        t1 = int(min(int64_t(n), t0 + (xe - x)));
+        x += t1 - t0;
+        whole = t1 - t0 == n;
+        i = e / a.row_tiles;
+        rt = e % a.row_tiles;
+    } else {
+        x = xe;
+        int64_t id = blockIdx.x;
+        rt = id % a.row_tiles;
+        id /= a.row_tiles;
+        h = int(id % H);
+        i = id / H;
+    }
     const Seq sq = seq_of(a.b, i);
     const int rows = sq.n * a.group;
-    if (rt * a.rows >= rows) return;
     const int r0 = int(rt) * a.rows;
+    if (r0 >= rows) break;  // (without shares only)
     const int64_t base = int64_t(sq.held) - sq.n;
     const Span sp = span_of(a, sq, r0);
-    int t0 = int(sp.lo), t1 = int(sp.hi);
-    if (a.splits > 1) {
-        t0 = int(min(sp.lo + split * a.split_tiles, sp.hi));
-        t1 = int(min(sp.hi, t0 + a.split_tiles));
-        if (t0 >= t1) return;  // no such part: the join counts the same parts
+    const int slot = a.items && t0 > 0 ? 2 * w : 2 * w + 1;
+    if (a.items) {
+        t0 += int(sp.lo);
+        t1 += int(sp.lo);
+    } else {
+        t0 = int(sp.lo);
+        t1 = int(sp.hi);
     }
     if (a.c.num_pages == 0) t1 = t0;
 
@@ -280,30 +381,34 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                 for (int k = 0; k < 8; ++k) v[k] += o_lds[w][q][d + k];
             }
             const int64_t at = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-            if (a.splits == 1) {
+            if (whole) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] *= inv;
                 store8<true>(static_cast<T*>(a.out) + at * D + d, v);
                 if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : mm * kLn2 + __logf(l);
             } else {
-                const int64_t pt = split * a.b.tokens * a.q_heads + at;
+                const int64_t pt = int64_t(slot) * a.rows + 16 * qt + q;
                 store8<true>(a.part_o + pt * D + d, v);
                 if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pt) = float2{mm, l};
             }
         }
         __syncthreads();
     }
+    }
 }
 
-// Joins a row's parts, in order: one workgroup a (token, head).
+// Joins rows' parts, in their order. Half a wave (a wave above headdim 128) takes a
+// row's parts, or `team` of them do where there are few rows (team: a power of two).
 template <typename T>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a) {
-    __shared__ float o_lds[4][256];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t at = blockIdx.x;
-    const int64_t tok = at / a.q_heads;
-    const int head = int(at - tok * a.q_heads);
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team) {
+    __shared__ __align__(16) float o_lds[256 * 4];
+    const int D = a.D, width = D <= 128 ? 32 : 64, crews = 256 / width;
+    const int crew = threadIdx.x / width, lane = threadIdx.x % width, member = crew % team;
+    const int64_t at = int64_t(blockIdx.x) * (crews / team) + crew / team;
+    bool live = at < a.b.tokens * a.q_heads;
+    const int64_t tok = live ? at / a.q_heads : 0;
+    const int head = live ? int(at - tok * a.q_heads) : 0;
     int64_t i = tok;
     if (a.b.cu_q) {  // the last sequence that begins at or before the row
         int64_t lo = 0, hi = a.b.batch - 1;
@@ -316,38 +421,74 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a) {
     }
     const Seq sq = seq_of(a.b, i);
     const int64_t t = tok - sq.row0;
-    if (t < 0 || t >= sq.n) return;
-    const int r = int(t) * a.group + head % a.group;
-    const Span sp = span_of(a, sq, r / a.rows * a.rows);
-    const int parts = int((sp.hi - sp.lo + a.split_tiles - 1) / a.split_tiles);
-    const int64_t step = a.b.tokens * a.q_heads;
+    live = live && t >= 0 && t < sq.n;
+    const int r = live ? int(t) * a.group + head % a.group : 0;
+    // part p of the row lies at p0 for p = 0, at p1 + p * step beyond
+    int64_t p0, p1, step;
+    int parts;
+    if (a.items) {
+        const int e = int(i * a.row_tiles) + r / a.rows, rin = r % a.rows;
+        const int share = a.shares[0], f = live ? a.shares[1 + e] : 0, n = live ? a.shares[2 + e] - f : 0;
+        const int64_t x0 = int64_t(a.c.heads) * f + int64_t(head / a.group) * n;
+        const int64_t w0 = x0 / share, w1 = (x0 + n - 1) / share;
+        parts = n ? int(w1 - w0) + 1 : 0;
+        live = parts > 1;  // else its workgroup wrote it (or it sees nothing)
+        p0 = (2 * w0 + 1) * a.rows + rin;
+        p1 = 2 * w0 * a.rows + rin;
+        step = 2 * a.rows;
+    } else {
+        const Span sp = live ? span_of(a, sq, r / a.rows * a.rows) : Span{0, 0};
+        parts = int((sp.hi - sp.lo + a.split_tiles - 1) / a.split_tiles);
+        p0 = p1 = at;
+        step = a.b.tokens * a.q_heads;
+    }
+    if (!live) parts = 0;
+    auto place = [&](int p) { return p ? p1 + p * step : p0; };
     float m = -INFINITY;
-    for (int p = lane; p < parts; p += 64) m = fmaxf(m, a.part_ml[2 * (p * step + at)]);
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    for (int p = lane; p < parts; p += width) m = fmaxf(m, a.part_ml[2 * place(p)]);
+    for (int x = 1; x < width; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
     float l = 0.f;
-    for (int p = lane; p < parts; p += 64) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * (p * step + at));
+    for (int p = lane; p < parts; p += width) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * place(p));
         l += ml.x == -INFINITY ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - m);
     }
-#pragma unroll
-    for (int x = 1; x < 64; x <<= 1) l += __shfl_xor(l, x);
-    const int D = a.D;
+    for (int x = 1; x < width; x <<= 1) l += __shfl_xor(l, x);
     floatx4 v{0, 0, 0, 0};
     if (4 * lane < D) {
 #pragma unroll 4
-        for (int p = wave; p < parts; p += 4) {
-            const float mp = a.part_ml[2 * (p * step + at)];
+        for (int p = member; p < parts; p += team) {
+            const float mp = a.part_ml[2 * place(p)];
             const float f = mp == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mp - m);
-            v += *reinterpret_cast<const floatx4*>(a.part_o + (p * step + at) * D + 4 * lane) * f;
+            v += *reinterpret_cast<const floatx4*>(a.part_o + place(p) * D + 4 * lane) * f;
         }
-        *reinterpret_cast<floatx4*>(&o_lds[wave][4 * lane]) = v;
     }
-    __syncthreads();
+    if (team > 1) {
+        *reinterpret_cast<floatx4*>(&o_lds[threadIdx.x * 4]) = v;
+        __syncthreads();
+        if (member == 0)
+            for (int k = 1; k < team; ++k) v += *reinterpret_cast<const floatx4*>(&o_lds[(threadIdx.x + k * width) * 4]);
+    }
+    if (!live || member) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int d = threadIdx.x; d < D; d += 256)
-        Io<T>::store(static_cast<T*>(a.out), at * D + d, (o_lds[0][d] + o_lds[1][d] + o_lds[2][d] + o_lds[3][d]) * inv);
-    if (a.lse && threadIdx.x == 0) a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + __logf(l);
+    if (4 * lane < D) {
+        T* out = static_cast<T*>(a.out) + at * D + 4 * lane;
+        if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<u32x2*>(out) = u32x2{pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv)};
+        else
+            *reinterpret_cast<floatx4*>(out) = v * inv;
+    }
+    if (a.lse && lane == 0) a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + __logf(l);
+}
+
+template <typename T>
+hipError_t launch_join(const AttendDev& d, hipStream_t s) {
+    const int64_t rows = d.b.tokens * d.q_heads;
+    const int crews = d.D <= 128 ? 8 : 4;
+    int team = 1;  // rows alone fill the chip from about 4 workgroups a CU
+    while (team < crews && rows * team / crews < 1024) team *= 2;
+    const int per = crews / team;
+    hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned((rows + per - 1) / per)), dim3(256), 0, s, d, team);
+    return hipGetLastError();
 }
 
 template <typename T, bool FP8, int DP, int QT>
@@ -363,14 +504,12 @@ hipError_t launch_attend(const AttendArgs& a) {
     const AttendPlan& p = a.plan;
     char* ws = static_cast<char*>(a.workspace);
     AttendDev d{a.c, a.b, a.q, a.out, a.lse, reinterpret_cast<float*>(ws + p.o_off),
-                reinterpret_cast<float*>(ws + p.ml_off), a.q_heads, a.q_heads / a.c.heads, a.c.headdim,
-                __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows, a.scale * kLog2e, a.causal, a.window, p.row_tiles,
-                p.split_tiles, p.splits, a.wide, a.b.batch * a.c.heads * p.row_tiles * p.splits};
+                reinterpret_cast<float*>(ws + p.ml_off), reinterpret_cast<int*>(ws), p.items, a.q_heads,
+                a.q_heads / a.c.heads, a.c.headdim, __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows,
+                a.scale * kLog2e, a.causal, a.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks};
     if (p.tile) {
-        hipError_t e = launch_attend_tile(d, a.io, a.stream);
-        if (e != hipSuccess || p.splits == 1) return e;
-        hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned(a.b.tokens * a.q_heads)), dim3(256), 0, a.stream, d);
-        return hipGetLastError();
+        const hipError_t e = launch_attend_tile(d, a.io, a.stream);
+        return e != hipSuccess || p.splits == 1 ? e : launch_join<T>(d, a.stream);
     }
     const int qt = p.rows / 16, dp = d.D <= 64 ? 64 : d.D <= 128 ? 128 : 256;
     if (dp == 64) {
@@ -382,10 +521,8 @@ hipError_t launch_attend(const AttendArgs& a) {
     } else {
         launch_rows<T, FP8, 256, 1>(d, a.stream);
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned(a.b.tokens * a.q_heads)), dim3(256), 0, a.stream, d);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !p.items ? e : launch_join<T>(d, a.stream);
 }
 
 }  // namespace
