@@ -9,10 +9,11 @@
 // head and the query heads, one job a wave at a time, dealt over blockIdx.y when
 // the blocks alone would leave the chip idle (single tokens).
 //
-// A job's rows go through the wave's own LDS rows in fp32: the maximum has to be
-// known before the first code, a rotation pairs entries of different lanes, and
-// V's codes lie transposed ([entry][token], so that attention reads 16 tokens of
-// an entry with one load). Waves never wait for each other after the angles.
+// The maximum has to be known before the first code, so a job holds its rows: wide
+// rows in registers, each lane pieces of 8 entries with their partners in the
+// rotation; V then crosses LDS once, as its codes lie transposed ([entry][token], so
+// that attention reads 16 tokens of an entry with one load). Other rows go through the
+// wave's own LDS rows in fp32. Waves never wait for each other after the angles.
 #include <algorithm>
 
 #include "m3_attn_device.h"
@@ -25,7 +26,9 @@ struct AppendDev {
     m3_kv_cache c;
     m3_kv_batch b;
     m3_rows k, v, q, qo;
-    int q_heads, D, half, interleaved, shift, nblk;
+    int q_heads, D, half, interleaved, shift, nblk, k_slices, v_slices;
+    int kq_jobs, v_jobs;      // register jobs of a row (0: the rows go through LDS)
+    unsigned kq_inv, v_inv;   // ceil(2^16 / jobs): e / jobs = e * inv >> 16 for e < 512
     float mscale;
     const float* inv_freq;
 };
@@ -77,6 +80,89 @@ __device__ __forceinline__ unsigned gather(const AppendDev& a, const T* src, int
     return top;
 }
 
+// A job's rows in registers. Job e of the (hi - lo) * jobs of the rows is piece
+// e % jobs (8 entries) of row e / jobs, or, with pairs (half layout), that piece and
+// its partner half further on; pieces after rot stand alone. A lane holds jobs lane,
+// lane + 64, ...; loads beyond the last job repeat it, so that none is behind a branch.
+// N: entries a lane holds, 32 for headdim up to 128, else 64.
+template <bool PAIRS, int N>
+struct Held {
+    static constexpr int kEach = PAIRS ? 16 : 8, kN = N / kEach;
+    float v[kN][kEach];
+};
+struct Job {
+    int s, d, two;  // row, first entry, whether the partner belongs to it
+};
+template <bool PAIRS>
+__device__ __forceinline__ Job job_of(const AppendDev& a, int e, int jobs, unsigned inv) {
+    const int s = int(unsigned(e) * inv >> 16), j = e - s * jobs;
+    if constexpr (PAIRS) {
+        const int turned = a.half / 8;
+        return Job{s, j < turned ? 8 * j : 8 * (j + turned), j < turned};
+    } else {
+        return Job{s, 8 * j, 0};
+    }
+}
+template <typename T, bool PAIRS, int N>
+__device__ __forceinline__ void fetch(const AppendDev& a, const T* src, int64_t tok, int n, int jobs, unsigned inv,
+                                      int lane, Held<PAIRS, N>& r) {
+#pragma unroll
+    for (int k = 0; k < (Held<PAIRS, N>::kN); ++k) {
+        if (64 * k >= n * jobs) break;  // (the wave as a whole)
+        const Job b = job_of<PAIRS>(a, min(lane + 64 * k, n * jobs - 1), jobs, inv);
+        const T* p = src + b.s * tok + b.d;
+        load8<true>(p, r.v[k]);
+        if constexpr (PAIRS) load8<true>(p + (b.two ? a.half : 0), r.v[k] + 8);
+    }
+}
+// turned by cs (rows lo ..), and the largest magnitude's bits
+template <bool PAIRS, int N>
+__device__ __forceinline__ unsigned turn_held(const AppendDev& a, const float2* cs, int n, int jobs, unsigned inv,
+                                              int lane, Held<PAIRS, N>& r) {
+    unsigned top = 0;
+#pragma unroll
+    for (int k = 0; k < (Held<PAIRS, N>::kN); ++k) {
+        if (64 * k >= n * jobs) break;
+        const Job b = job_of<PAIRS>(a, min(lane + 64 * k, n * jobs - 1), jobs, inv);
+        float* v = r.v[k];
+        if constexpr (PAIRS) {
+            if (cs && b.two) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float2 w = cs[b.s * a.half + b.d + x];
+                    turn(v[x], v[8 + x], w.x, w.y);
+                }
+            }
+#pragma unroll
+            for (int x = 8; x < 16; ++x) top = max(top, mag(v[x]));  // (alone: the piece twice)
+        } else if (cs && b.d < 2 * a.half) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 w = cs[b.s * a.half + b.d / 2 + x];
+                turn(v[2 * x], v[2 * x + 1], w.x, w.y);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) top = max(top, mag(v[x]));
+        __builtin_amdgcn_sched_barrier(0);  // (one job's angles at a time)
+    }
+    return top;
+}
+// What a job does with each piece it holds: at(row, first entry, 8 values).
+template <bool PAIRS, int N, typename F>
+__device__ __forceinline__ void each_piece(const AppendDev& a, int n, int jobs, unsigned inv, int lane, Held<PAIRS, N>& r,
+                                           F at) {
+#pragma unroll
+    for (int k = 0; k < (Held<PAIRS, N>::kN); ++k) {
+        const int e = lane + 64 * k;
+        if (e >= n * jobs) continue;
+        const Job b = job_of<PAIRS>(a, e, jobs, inv);
+        at(b.s, b.d, r.v[k]);
+        if constexpr (PAIRS)
+            if (b.two) at(b.s, b.d + a.half, r.v[k] + 8);
+    }
+}
+
 // The scale of a block from its old one and the largest new magnitude.
 struct Scale {
     float s, inv;  // stored scale; 1 / s, or 0 where nothing can be held (s 0 or not finite)
@@ -115,91 +201,167 @@ __device__ __forceinline__ u32x4 recode16(u32x4 w, float ratio) {
     return w;
 }
 
-template <typename T, bool FP8, bool WIDE>
-__global__ void append_kernel(AppendDev a) {
+// A workgroup's block: slots lo .. hi - 1 of it are new, row the batch's row of the
+// first, at its index in the cache (head 0; -1: no page), begun: it holds older tokens.
+struct Where {
+    int lo, hi;
+    int64_t row, at;
+    bool begun;
+};
+
+template <typename T, bool WIDE, int REG, int N>
+__device__ __forceinline__ void put_query(const AppendDev& a, const Where& w, int h, const float2* cs, float* rows,
+                                          int lane) {
+    const T* src = static_cast<const T*>(a.q.p) + w.row * a.q.token_stride + h * a.q.head_stride;
+    T* dst = static_cast<T*>(a.qo.p) + w.row * a.qo.token_stride + h * a.qo.head_stride;
+    const int n = w.hi - w.lo, D = a.D;
+    if constexpr (REG > 0) {
+        Held<REG == 2, N> r;
+        fetch<T>(a, src, a.q.token_stride, n, a.kq_jobs, a.kq_inv, lane, r);
+        turn_held(a, cs ? cs + w.lo * a.half : nullptr, n, a.kq_jobs, a.kq_inv, lane, r);
+        each_piece(a, n, a.kq_jobs, a.kq_inv, lane, r,
+                   [&](int s, int d, const float* v) { store8<true>(dst + s * a.qo.token_stride + d, v); });
+    } else {
+        gather<T, WIDE>(a, src, a.q.token_stride, w.lo, w.hi, rows, cs, lane);
+        for (int e = lane; e < n * (D / 8); e += 64) {
+            const int s = e / (D / 8), d = 8 * (e - s * (D / 8));
+            store8<WIDE>(dst + s * a.qo.token_stride + d, rows + (w.lo + s) * D + d);
+        }
+        wave_fence();
+    }
+}
+
+template <typename T, bool FP8, bool WIDE, int REG, int N>
+__device__ __forceinline__ void put_key(const AppendDev& a, const Where& w, int h, const float2* cs, float* rows,
+                                        int lane) {
+    const int64_t slot = w.at + (int64_t(h) << a.shift);
+    const int lo = w.lo, hi = w.hi, n = hi - lo, D = a.D, per = D / 16;
+    char* code = static_cast<char*>(a.c.k) + slot * 16 * D;
+    const T* src = static_cast<const T*>(a.k.p) + w.row * a.k.token_stride + h * a.k.head_stride;
+    const float old = w.begun ? a.c.k_scale[slot] : 0.f;
+    unsigned top;
+    Held<REG == 2, N> r;
+    if constexpr (REG > 0) {
+        fetch<T>(a, src, a.k.token_stride, n, a.kq_jobs, a.kq_inv, lane, r);
+        top = turn_held(a, cs ? cs + lo * a.half : nullptr, n, a.kq_jobs, a.kq_inv, lane, r);
+    } else {
+        top = gather<T, WIDE>(a, src, a.k.token_stride, lo, hi, rows, cs, lane);
+    }
+    const Scale ns = new_scale<FP8>(old, wave_umax(top));
+    const bool none = ns.inv == 0.f, all = !w.begun || __float_as_uint(ns.s) != __float_as_uint(old);
+    if constexpr (REG > 0) {
+        each_piece(a, n, a.kq_jobs, a.kq_inv, lane, r, [&](int s, int d, const float* v) {
+            const float i = ns.inv;
+            u32x2 c{Code<FP8>::enc4(v[0] * i, v[1] * i, v[2] * i, v[3] * i),
+                    Code<FP8>::enc4(v[4] * i, v[5] * i, v[6] * i, v[7] * i)};
+            if (none) c = u32x2{0, 0};
+            *reinterpret_cast<u32x2*>(code + (lo + s) * D + d) = c;
+        });
+    } else {
+        for (int e = lane; e < n * per; e += 64) {
+            const int s = lo + e / per, d = 16 * (e % per);
+            *reinterpret_cast<u32x4*>(code + s * D + d) =
+                none ? u32x4{0, 0, 0, 0} : codes16<FP8>(rows + s * D + d, 1, ns.inv);
+        }
+    }
+    if (all) {  // the other slots too: older codes where the scale grew, 0 after the end
+        const float ratio = none ? 0.f : old * ns.inv;
+        for (int e = lane; e < (16 - n) * per; e += 64) {
+            const int f = e / per, s = f < lo ? f : f + n;
+            u32x4* c = reinterpret_cast<u32x4*>(code + s * D + 16 * (e % per));
+            *c = s < lo && !none ? recode16<FP8>(*c, ratio) : u32x4{0, 0, 0, 0};
+        }
+    }
+    if (lane == 0) a.c.k_scale[slot] = ns.s;
+    wave_fence();
+}
+
+template <typename T, bool FP8, bool WIDE, int REG, int N>
+__device__ __forceinline__ void put_value(const AppendDev& a, const Where& w, int h, float* rows, int lane) {
+    const int64_t slot = w.at + (int64_t(h) << a.shift);
+    const int lo = w.lo, hi = w.hi, n = hi - lo, D = a.D;
+    u32x4* code = reinterpret_cast<u32x4*>(static_cast<char*>(a.c.v) + slot * 16 * D);
+    const T* src = static_cast<const T*>(a.v.p) + w.row * a.v.token_stride + h * a.v.head_stride;
+    const float old = w.begun ? a.c.v_scale[slot] : 0.f;
+    unsigned top;
+    if constexpr (REG > 0) {
+        Held<false, N> r;
+        fetch<T>(a, src, a.v.token_stride, n, a.v_jobs, a.v_inv, lane, r);
+        top = turn_held(a, static_cast<const float2*>(nullptr), n, a.v_jobs, a.v_inv, lane, r);
+        each_piece(a, n, a.v_jobs, a.v_inv, lane, r,
+                   [&](int s, int d, const float* v) { store8<true>(rows + (lo + s) * D + d, v); });
+        wave_fence();
+    } else {
+        top = gather<T, WIDE>(a, src, a.v.token_stride, lo, hi, rows, nullptr, lane);
+    }
+    const Scale ns = new_scale<FP8>(old, wave_umax(top));
+    const bool none = ns.inv == 0.f, grown = __float_as_uint(ns.s) != __float_as_uint(old);
+    const float ratio = none ? 0.f : old * ns.inv;
+    // 16 slots of one entry a lane; old slots keep their byte unless the scale grew
+    for (int d = lane; d < D; d += 64) {
+        u32x4 c = w.begun ? code[d] : u32x4{0, 0, 0, 0};
+        if (w.begun && grown) c = none ? u32x4{0, 0, 0, 0} : recode16<FP8>(c, ratio);
+        const u32x4 f = none ? u32x4{0, 0, 0, 0} : codes16<FP8>(rows + d, D, ns.inv);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const int l = min(max(lo - 4 * b, 0), 4), u = min(max(hi - 4 * b, 0), 4);
+            const unsigned below = l == 4 ? ~0u : (1u << (8 * l)) - 1u;
+            const unsigned upto = u == 4 ? ~0u : (1u << (8 * u)) - 1u;
+            c[b] = (c[b] & below) | (f[b] & upto & ~below);
+        }
+        code[d] = c;
+    }
+    if (lane == 0) a.c.v_scale[slot] = ns.s;
+    wave_fence();
+}
+
+// REG: 0 the rows go through LDS (any rotation, stride and alignment); 1, 2 wide rows
+// held in registers, single pieces or pairs. blockIdx.y: slices of the key heads, then
+// of the value heads, then of the query heads (a loop of its own each, or their
+// invariants would all be held at once).
+template <typename T, bool FP8, bool WIDE, int REG, int N>
+__global__ __launch_bounds__(256, REG ? (N == 32 ? 4 : 2) : 1) void append_kernel(AppendDev a) {
     extern __shared__ __align__(16) float lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int64_t i = blockIdx.x / a.nblk;
     const Seq q = seq_of(a.b, i);
     const int64_t before = int64_t(q.held) - q.n;  // position of the sequence's first row (negative: not stored)
     const int64_t blk = (before >> 4) + int(blockIdx.x % a.nblk);
-    const int lo = int(max(before - 16 * blk, int64_t(0)));
-    const int hi = int(min(int64_t(q.held) - 16 * blk, int64_t(16)));  // slots lo .. hi - 1 are new
-    if (hi <= lo) return;                          // (the workgroup as a whole)
-    const int64_t row = q.row0 + (16 * blk + lo - before);
+    Where w;
+    w.lo = int(max(before - 16 * blk, int64_t(0)));
+    w.hi = int(min(int64_t(q.held) - 16 * blk, int64_t(16)));
+    if (w.hi <= w.lo) return;  // (the workgroup as a whole)
+    w.row = q.row0 + (16 * blk + w.lo - before);
+    w.begun = w.lo > 0 && blk * 16 < before;
+    w.at = block_at(a.b.pages + i * a.b.max_pages, a.b.max_pages, a.c.num_pages, a.shift, a.c.heads, blk);
 
     float* rows = lds + wave * 16 * a.D;
+    const int y = blockIdx.y;
+    if (y >= a.k_slices && y < a.k_slices + a.v_slices) {
+        if (w.at >= 0)
+            for (int h = (y - a.k_slices) * waves + wave; h < a.c.heads; h += a.v_slices * waves)
+                put_value<T, FP8, WIDE, REG, N>(a, w, h, rows, lane);
+        return;
+    }
     float2* cs = nullptr;
     if (a.inv_freq) {
         cs = reinterpret_cast<float2*>(lds + waves * 16 * a.D);
-        for (int e = threadIdx.x; e < (hi - lo) * a.half; e += blockDim.x) {
+        for (int e = threadIdx.x; e < (w.hi - w.lo) * a.half; e += blockDim.x) {
             const int s = e / a.half, p = e - s * a.half;
             float c, sn;
-            cos_sin(int32_t(16 * blk + lo + s), a.inv_freq[p], double(a.mscale), &c, &sn);
-            cs[(lo + s) * a.half + p] = float2{c, sn};
+            cos_sin(int32_t(16 * blk + w.lo + s), a.inv_freq[p], double(a.mscale), &c, &sn);
+            cs[(w.lo + s) * a.half + p] = float2{c, sn};
         }
         __syncthreads();
     }
-    const int H = a.c.heads, D = a.D;
-    const int64_t at = block_at(a.b.pages + i * a.b.max_pages, a.b.max_pages, a.c.num_pages, a.shift, H, blk);
-    const bool begun = lo > 0 && blk * 16 < before;
-    for (int j = blockIdx.y * waves + wave; j < 2 * H + a.q_heads; j += gridDim.y * waves) {
-        if (j >= 2 * H) {  // a query head
-            const int h = j - 2 * H;
-            const T* src = static_cast<const T*>(a.q.p) + row * a.q.token_stride + h * a.q.head_stride;
-            T* dst = static_cast<T*>(a.qo.p) + row * a.qo.token_stride + h * a.qo.head_stride;
-            gather<T, WIDE>(a, src, a.q.token_stride, lo, hi, rows, cs, lane);
-            for (int e = lane; e < (hi - lo) * (D / 8); e += 64) {
-                const int s = e / (D / 8), d = 8 * (e - s * (D / 8));
-                store8<WIDE>(dst + s * a.qo.token_stride + d, rows + (lo + s) * D + d);
-            }
-            wave_fence();
-            continue;
-        }
-        if (at < 0) continue;
-        const bool is_v = j >= H;
-        const int h = is_v ? j - H : j;
-        const m3_rows& r = is_v ? a.v : a.k;
-        const int64_t slot = at + (int64_t(h) << a.shift);
-        float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + slot;
-        u32x4* code = reinterpret_cast<u32x4*>(static_cast<char*>(is_v ? a.c.v : a.c.k) + slot * 16 * D);
-        const float old = begun ? *scale : 0.f;
-        const T* src = static_cast<const T*>(r.p) + row * r.token_stride + h * r.head_stride;
-        const unsigned top = wave_umax(gather<T, WIDE>(a, src, r.token_stride, lo, hi, rows, is_v ? nullptr : cs, lane));
-        const Scale ns = new_scale<FP8>(old, top);
-        const bool grown = __float_as_uint(ns.s) != __float_as_uint(old);
-        const float ratio = ns.inv == 0.f ? 0.f : old * ns.inv;
-        const bool none = ns.inv == 0.f;
-        if (is_v) {
-            // 16 slots of one entry a lane; old slots keep their byte unless the scale grew
-            for (int d = lane; d < D; d += 64) {
-                u32x4 w = begun ? code[d] : u32x4{0, 0, 0, 0};
-                if (begun && grown) w = none ? u32x4{0, 0, 0, 0} : recode16<FP8>(w, ratio);
-                const u32x4 f = none ? u32x4{0, 0, 0, 0} : codes16<FP8>(rows + d, D, ns.inv);
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int l = min(max(lo - 4 * b, 0), 4), u = min(max(hi - 4 * b, 0), 4);
-                    const unsigned below = l == 4 ? ~0u : (1u << (8 * l)) - 1u;
-                    const unsigned upto = u == 4 ? ~0u : (1u << (8 * u)) - 1u;
-                    w[b] = (w[b] & below) | (f[b] & upto & ~below);
-                }
-                code[d] = w;
-            }
-        } else {
-            // a row of D codes a slot: the new ones, and all 16 where the block begins or the scale grew
-            const int s0 = begun && !grown ? lo : 0, s1 = begun && !grown ? hi : 16, per = D / 16;
-            for (int e = lane; e < (s1 - s0) * per; e += 64) {
-                const int s = s0 + e / per, d = e % per;
-                u32x4 w{0, 0, 0, 0};
-                if (!none && s < lo)
-                    w = begun ? recode16<FP8>(code[s * per + d], ratio) : w;
-                else if (!none && s < hi)
-                    w = codes16<FP8>(rows + s * D + 16 * d, 1, ns.inv);
-                code[s * per + d] = w;
-            }
-        }
-        if (lane == 0) *scale = ns.s;
-        wave_fence();
+    if (y < a.k_slices) {
+        if (w.at >= 0)
+            for (int h = y * waves + wave; h < a.c.heads; h += a.k_slices * waves)
+                put_key<T, FP8, WIDE, REG, N>(a, w, h, cs, rows, lane);
+    } else {
+        const int first = a.k_slices + a.v_slices, q_slices = gridDim.y - first;
+        for (int h = (y - first) * waves + wave; h < a.q_heads; h += q_slices * waves)
+            put_query<T, WIDE, REG, N>(a, w, h, cs, rows, lane);
     }
 }
 
@@ -207,18 +369,34 @@ template <typename T, bool FP8>
 hipError_t launch_append(const AppendArgs& a) {
     AppendDev d{a.c, a.b, a.k, a.v, a.q, a.q_out, a.q.p ? a.q_heads : 0, a.c.headdim, a.rot.rot / 2,
                 a.rot.interleaved, __builtin_ctz(unsigned(a.c.page_size / 16)), int((a.b.max_q + 14) / 16 + 1),
-                a.rot.mscale, a.rot.inv_freq};
+                0, 0, 0, 0, 0, 0, a.rot.mscale, a.rot.inv_freq};
+    const int D = a.c.headdim, rot = a.rot.inv_freq ? a.rot.rot : 0;
+    const bool pairs = rot && !a.rot.interleaved;
+    int reg = a.wide && rot % (pairs ? 16 : 8) == 0 ? (pairs ? 2 : 1) : 0;
+    d.kq_jobs = pairs ? (D - rot / 2) / 8 : D / 8;
+    if (reg == 2 && d.kq_jobs > (D <= 128 ? 8 : 16)) reg = 0;  // (a short rotated part of a wide head: too many registers as pairs)
+    d.v_jobs = D / 8;
+    d.kq_inv = (65536u + d.kq_jobs - 1) / d.kq_jobs;
+    d.v_inv = (65536u + d.v_jobs - 1) / d.v_jobs;
     const int64_t blocks = a.b.batch * d.nblk;
     const int waves = a.c.headdim <= 128 ? 4 : 2;  // LDS rows and angles within 64 KiB
-    const int jobs = 2 * a.c.heads + d.q_heads;
-    // as many slices of the jobs as leave about 4 workgroups a CU
-    const int slices = int(std::max<int64_t>(1, std::min<int64_t>((jobs + waves - 1) / waves, 1024 / blocks)));
+    // heads of a wave: 1, or as many as leave about 8 workgroups a CU
+    const int64_t wide = blocks * (2 * a.c.heads + d.q_heads);
+    const int each = int(std::min<int64_t>(16, std::max<int64_t>(1, wide / (2048 * waves))));
+    auto slices = [&](int heads) { return (heads + waves * each - 1) / (waves * each); };
+    d.k_slices = d.v_slices = slices(a.c.heads);
+    const int y = 2 * d.k_slices + slices(d.q_heads);
     const size_t lds = size_t(waves) * 16 * a.c.headdim * 4 + (a.rot.inv_freq ? size_t(16) * d.half * 8 : 0);
-    const dim3 grid{unsigned(blocks), unsigned(slices)}, block{unsigned(64 * waves)};
-    if (a.wide)
-        hipLaunchKernelGGL((append_kernel<T, FP8, true>), grid, block, lds, a.stream, d);
+    const dim3 grid{unsigned(blocks), unsigned(y)}, block{unsigned(64 * waves)};
+    auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, a.stream, d); };
+    if (reg == 2)
+        D <= 128 ? launch(append_kernel<T, FP8, true, 2, 32>) : launch(append_kernel<T, FP8, true, 2, 64>);
+    else if (reg == 1)
+        D <= 128 ? launch(append_kernel<T, FP8, true, 1, 32>) : launch(append_kernel<T, FP8, true, 1, 64>);
+    else if (a.wide)
+        launch(append_kernel<T, FP8, true, 0, 32>);
     else
-        hipLaunchKernelGGL((append_kernel<T, FP8, false>), grid, block, lds, a.stream, d);
+        launch(append_kernel<T, FP8, false, 0, 32>);
     return hipGetLastError();
 }
 
