@@ -11,8 +11,9 @@
 // registers while this tile is computed, and are written to the other image
 // before the one barrier of a tile.
 //
-// The running reference is raised (and the sums scaled) only when a score passes it
-// by 2^8, which fp16 still holds, so the O^T registers are mostly left alone.
+// A tile's probabilities are formed with the reference as it stands, beside the next
+// tile's scores; only where one leaves fp16's range is the maximum taken, the sums
+// scaled and the tile's probabilities formed again. No maximum is needed otherwise.
 #include <algorithm>
 
 #include "m3_attend_common.h"
@@ -21,13 +22,14 @@ namespace m3 {
 namespace {
 
 template <typename T, bool FP8, int DP, int QT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KM = DP / 32;          // MFMA steps of a score (32 entries each)
     constexpr int DT = DP / 16;
     constexpr int NT = 64 * NW;
     constexpr int PC = 4 * DP / NT;      // 16-code pieces of K, and of V, a thread brings
     static_assert(PC >= 1 && 4 * DP % NT == 0, "threads and pieces");
+    constexpr bool kAhead = DP > 64;
     constexpr int KB = 64 * DP * 2;      // bytes of K's, and of V's, image
     extern __shared__ __align__(16) char lds[];  // two K images, two V images
     __shared__ float sc_lds[2][4][4];    // of the tile's blocks: K scale, log2 and inverse of V's, whether held
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
     float mx[QT], sum[QT];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
-        mx[qt] = -INFINITY;
+        mx[qt] = wr0 + 16 * qt + lr < rows ? -INFINITY : 0.f;
         sum[qt] = 0.f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
@@ -221,9 +223,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
     };
     auto seen = [&](int tile) { return tile * kTile < w_hi && tile * kTile + kTile > w_lo; };
 
-    // In turn n: the scores of tile n are in registers, V of tile n and K of tile n + 1
-    // in LDS. The products of tile n + 1's scores run beside tile n's exponentials, those
-    // with V beside the conversion of what comes next (K of n + 2, V of n + 1).
+    // kAhead. In turn n the scores of tile n are in registers, V of tile n and K of tile
+    // n + 1 in LDS: the products of tile n + 1's scores run beside tile n's exponentials,
+    // those with V beside the conversion of what comes next (K of n + 2, V of n + 1).
+    // Headdim 64 has half the products for as many exponentials: there three waves a SIMD
+    // without the second set of scores do better (K and V of n + 1 are converted in turn n).
     Pages pgv{}, pgk{};
     if (t0 < t1) {
         pgk = find(t0);
@@ -232,26 +236,33 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
         pgv = find(t0 + 1);
         stage_k(0);
         stage_v(t0, 0);
-        fetch_k(t0 + 1, pgv);
-        pgk = find(t0 + 2);
-        stage_k(1);
-        __syncthreads();
-        if (seen(t0)) scores(0, s);
+        if constexpr (kAhead) {
+            fetch_k(t0 + 1, pgv);
+            pgk = find(t0 + 2);
+            stage_k(1);
+            __syncthreads();
+            if (seen(t0)) scores(0, s);
+        }
         __syncthreads();
     }
-    int buf = 0;
-    for (int tile = t0; tile < t1; ++tile, buf ^= 1) {
-        fetch_k(tile + 2, pgk);  // (nothing after the last)
-        fetch_v(tile + 1, pgv);
-        pgv = pgk;
-        pgk = find(tile + 3);
+    bool started = false;  // every row of the wave has a reference
+    auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4]) {
+        fetch_v(tile + 1, pgv);  // (nothing after the last)
+        if constexpr (kAhead) {
+            fetch_k(tile + 2, pgk);
+            pgv = pgk;
+            pgk = find(tile + 3);
+        } else {
+            fetch_k(tile + 1, pgv);
+            pgv = find(tile + 2);
+        }
         const int k0 = tile * kTile;
         if (seen(tile)) {
+            if constexpr (!kAhead) scores(buf, s);
             const floatx4 sc = *reinterpret_cast<const floatx4*>(sc_lds[buf][g]);
             float ks = sc[0], lv = sc[1];
             const float iv = sc[2];
-            // (a scale below 0 would turn the raw maximum round)
-            if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f || !(ks >= 0.f))) {
+            if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
@@ -263,49 +274,62 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
                 ks = 1.f;
                 lv = 0.f;
             }
-            float c[QT];
-            bool up = false;
+            u32x4 pf[QT][2][NV];
+            float add[QT], big = 0.f;
+            auto part = [&](int x, float c) {  // probability x % 16 of row tile x / 16
+                const int qt = x / 16, j = x % 16;
+                return __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c));
+            };
+            auto close = [&](int qt, const float* p) {
+                add[qt] = 0.f;
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-                float top = s[qt][0][0];
+                for (int j = 0; j < 16; ++j) add[qt] += p[j];
+                pack_p<NV>(p, pf[qt]);
+            };
+            {
+                float p[QT][16], c[QT];
 #pragma unroll
-                for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
-                c[qt] = quad_max(__builtin_fmaf(top, ks, lv)) - kUp;
-                up |= c[qt] > mx[qt] + kSlack;
-            }
-            if (__any(up)) {
+                for (int qt = 0; qt < QT; ++qt) c[qt] = lv - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
+                constexpr int kSteps = 4 * KM;
+#pragma unroll
+                for (int u = 0; u < kSteps; ++u) {
+                    if constexpr (kAhead) score_step(buf ^ 1, u / KM, u % KM, sn);
+#pragma unroll
+                    for (int x = u * 16 * QT / kSteps; x < (u + 1) * 16 * QT / kSteps; ++x) p[x / 16][x % 16] = part(x, c[x / 16]);
+                }
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
-                    const float m2 = fmaxf(mx[qt], c[qt]);
+                    close(qt, p[qt]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) big = fmaxf(big, p[qt][j]);
+                }
+            }
+            // From 2^15 on, or before the first reference, the exact maximum is taken and all
+            // of this tile's probabilities are formed again. (No short cut past `started`:
+            // the arithmetic would move behind it, away from the products it runs beside.)
+            if (__any(int(!started) | int(big >= kF16Top))) {
+                started = true;
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) top = fmaxf(top, __builtin_fmaf(s[qt][j / 4][j % 4], ks, lv));
+                    const float m2 = fmaxf(mx[qt], quad_max(top) - kUp);
                     const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
                     mx[qt] = m2;
                     sum[qt] *= fade;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
-                }
-            }
-            u32x4 pf[QT][2][NV];
-            float p[QT][16];
+                    const float c = lv - (m2 == -INFINITY ? 0.f : m2);
+                    float p[16];
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) c[qt] = lv - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
-            constexpr int kSteps = 4 * KM;
-#pragma unroll
-            for (int u = 0; u < kSteps; ++u) {
-                score_step(buf ^ 1, u / KM, u % KM, sn);
-#pragma unroll
-                for (int x = u * 16 * QT / kSteps; x < (u + 1) * 16 * QT / kSteps; ++x) {  // its share
-                    const int qt = x / 16, j = x % 16;
-                    p[qt][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c[qt]));
+                    for (int j = 0; j < 16; ++j) p[j] = part(16 * qt + j, c);
+                    close(qt, p);
+                    started = started && !__any(m2 == -INFINITY);
                 }
             }
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-                float add = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) add += p[qt][j];
-                sum[qt] += add == 0.f ? 0.f : add * iv;  // (a block no row sees may hold NaN)
-                pack_p<NV>(p[qt], pf[qt]);
-            }
+            for (int qt = 0; qt < QT; ++qt) sum[qt] += add[qt] == 0.f ? 0.f : add[qt] * iv;  // (a block no row sees may hold NaN)
             const char* vi = lds + (2 + buf) * KB + lane * 16;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -317,16 +341,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attend_tile_kernel(AttendDev a) {
 #pragma unroll
                         for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
                 }
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
-#pragma unroll
-                for (int t = 0; t < 4; ++t) s[qt][t] = sn[qt][t];
-        } else if (seen(tile + 1)) {
-            scores(buf ^ 1, s);
+        } else if (kAhead && seen(tile + 1)) {
+            scores(buf ^ 1, sn);
         }
-        stage_k(buf);
+        stage_k(kAhead ? buf : buf ^ 1);
         stage_v(tile + 1, buf ^ 1);
         __syncthreads();
+    };
+    for (int tile = t0; tile < t1; tile += 2) {
+        turn_of(tile, 0, s, sn);
+        if (tile + 1 < t1) {
+            if constexpr (kAhead) turn_of(tile + 1, 1, sn, s);
+            else turn_of(tile + 1, 1, s, sn);
+        }
     }
 
 #pragma unroll

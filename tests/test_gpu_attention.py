@@ -429,6 +429,25 @@ def test_attend_scale_and_peaks():
         bench.attend(q, [4], io, scale=-0.3)
 
 
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_attend_scores_that_jump(rows, dim, io):
+    """One key a sequence, each place of a tile in turn, lies 2^58 above all before it; then the scores fall again.
+    (Blocks share a scale, so the loud key's neighbours lose their small values: the reference reads what is held.)"""
+    L, at = 200, torch.arange(64) + 64
+    bench = Bench(64, 1, dim, 16, 208, F8, seed=dim)
+    u = torch.zeros(dim)
+    u[::8] = 1.0
+    k = 0.05 * normal(bench.g, 64, L, 1, dim)
+    k[torch.arange(64), at, 0] += 40.0 / (dim / 8) * u
+    k[:, 170:] -= 3.0 / (dim / 8) * u
+    v = normal(bench.g, 64, L, 1, dim)
+    bench.append([L] * 64, rows=(k.reshape(-1, 1, dim), v.reshape(-1, 1, dim)))
+    q = (u + 0.05 * normal(bench.g, 64 * rows, 2, dim)).to(io)
+    bench.attend(q, [rows] * 64, io, scale=1.0)
+
+
 def test_attend_missing_pages():
     """Keys of pages outside the pool are absent, at the start, inside, and all of a sequence's."""
     for n in ([1, 1, 1], [40, 130, 20]):
