@@ -163,10 +163,12 @@ namespace m3 {
 // tiles of 64 a workgroup, while there are fewer row tiles than two a CU. Else rows of
 // a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
 // twice the rows; at headdim above 128 the registers hold 16). A row tile and key head
-// is a workgroup's where that makes two workgroups a CU (128 sequences of 2112 tokens, 4
-// heads: 56 us, 66 by even shares and their join; of 127 .. 4095 tokens: 73 and 77) or
-// every sequence is short (8 tiles: two a wave); else all tiles are dealt out in even
-// shares, which a loose max_kv does not hurt.
+// is a workgroup's where that fills the chip (two workgroups a CU, one above headdim
+// 128: 128 sequences of 2112 tokens, 4 heads, 54 us and 66 by even shares with their
+// join; of 127 .. 4095 tokens 71 and 77) or every sequence is short (16 tiles: 64
+// sequences of 701 tokens 15 and 26 us); else all tiles are dealt out in even shares
+// (64 sequences of 200 .. 8000 tokens: 68 us, 109 without), which a loose max_kv does
+// not hurt.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
     (void)causal;
@@ -190,9 +192,10 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
         p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
         p.blocks = base * p.splits;
         if (p.splits > 1) parts = size_t(p.splits) * size_t(b.tokens) * size_t(q_heads);
-    } else if (tiles > 8 && base < 512 && items <= kAttendItems && items * tiles <= INT32_MAX) {
+    } else if (const int64_t full = width == 2 ? 256 : 512;
+               tiles > 16 && base < full && items <= kAttendItems && items * tiles <= INT32_MAX) {
         p.items = int32_t(items);
-        p.blocks = std::min<int64_t>(512, (base * tiles + 3) / 4);
+        p.blocks = std::min<int64_t>(full, (base * tiles + 3) / 4);
         parts = size_t(2 * p.blocks) * size_t(p.rows);
         p.o_off = (size_t(items + 2) * 4 + 255) / 256 * 256;
     }

@@ -106,7 +106,9 @@ __device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) 
 }
 
 // FULL: headdim is DP, so that every piece is there and loads have constant offsets.
-template <typename T, bool FP8, int DP, int QT, bool FULL>
+// EVEN: even shares (their bookkeeping takes registers that the other case keeps for
+// more waves).
+template <typename T, bool FP8, int DP, int QT, bool FULL, bool EVEN>
 __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * QT > 128) ? 1 : 2) void attend_rows_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KC = DP / 64;        // 16-code pieces of a key row a lane holds
@@ -118,21 +120,21 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, g = lane >> 4;
     const int H = a.c.heads;
-    __shared__ int first_lds[kMaxItems + 1];
+    __shared__ int first_lds[EVEN ? kMaxItems + 1 : 1];
     __shared__ int scan_lds[kWaves];
-    int share = 0, w = blockIdx.x;  // tiles of a share; this one
-    int64_t x = 0, xe = 1;          // what is left of it
-    if (a.items) {
-        share = even_shares(a, first_lds, scan_lds);
+    const int w = blockIdx.x;
+    int64_t x = 0, xe = 1;  // what is left of this workgroup's share
+    if constexpr (EVEN) {
+        const int share = even_shares(a, first_lds, scan_lds);
         x = int64_t(w) * share;
         xe = min(x + share, int64_t(H) * first_lds[a.items]);
         zero_rows<T>(a, first_lds);
     }
     while (x < xe) {  // (a share may end one row tile's keys and begin the next's)
     int64_t i, rt;
-    int h, t0, t1;
+    int h, t0 = 0, t1 = 0;
     bool whole = true;
-    if (a.items) {
+    if constexpr (EVEN) {
         int e = 0;
         for (int hi = a.items - 1; e < hi;) {  // the last item that begins at or before x
             const int mid = (e + hi + 1) / 2;
@@ -150,11 +152,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
         rt = e % a.row_tiles;
     } else {
         x = xe;
-        int64_t id = blockIdx.x;
-        rt = id % a.row_tiles;
-        id /= a.row_tiles;
-        h = int(id % H);
-        i = id / H;
+        rt = w % a.row_tiles;
+        const int64_t ih = w / a.row_tiles;
+        h = int(ih % H);
+        i = ih / H;
     }
     const Seq sq = seq_of(a.b, i);
     const int rows = sq.n * a.group;
@@ -162,8 +163,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
     if (r0 >= rows) break;  // (without shares only)
     const int64_t base = int64_t(sq.held) - sq.n;
     const Span sp = span_of(a, sq, r0);
-    const int slot = a.items && t0 > 0 ? 2 * w : 2 * w + 1;
-    if (a.items) {
+    const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
+    if constexpr (EVEN) {
         t0 += int(sp.lo);
         t1 += int(sp.lo);
     } else {
@@ -198,11 +199,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             }
     };
     int tile = t0 + wave;
-    int kb = -1, vb = -1;
+    int vb = -1;
     if (tile < t1) {
-        kb = find(tile * 4 + (lr >> 2));
         vb = find(tile * 4 + g);
-        load_k(kb);
+        load_k(find(tile * 4 + (lr >> 2)));
     }
 
     // the rows' operands and the keys that each row sees
@@ -279,8 +279,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const int key = k0 + 16 * g + j;
-                    const float v = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
-                    s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
+                    const float x = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
+                    s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? x : -INFINITY;
                 }
             ks = 1.f;
             vs.log2 = 0.f;
@@ -340,7 +340,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                     for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
                 if (hf && d % 2) __builtin_amdgcn_sched_barrier(0);
             }
-        kb = kb2;
         vb = vb2;
     }
 
@@ -493,11 +492,15 @@ hipError_t launch_join(const AttendDev& d, hipStream_t s) {
 
 template <typename T, bool FP8, int DP, int QT>
 void launch_rows(const AttendDev& d, hipStream_t s) {
-    const dim3 grid(unsigned(d.blocks)), block(64 * kWaves);
-    if (d.D == DP)
-        hipLaunchKernelGGL((attend_rows_kernel<T, FP8, DP, QT, true>), grid, block, 0, s, d);
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(unsigned(d.blocks)), dim3(64 * kWaves), 0, s, d);
+    };
+    if (d.items)
+        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, true>)
+                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, true>);
     else
-        hipLaunchKernelGGL((attend_rows_kernel<T, FP8, DP, QT, false>), grid, block, 0, s, d);
+        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, false>)
+                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, false>);
 }
 template <typename T, bool FP8>
 hipError_t launch_attend(const AttendArgs& a) {

@@ -191,7 +191,7 @@ def test_workspace_size(lib, b, h, kv, max_q, max_kv):
     n = lib.m3_kv_attend_workspace_size(c, bt, h, 1, 1, 0)
     part = 128 * 4 + 8
     assert n <= max(1024 * 32, 64 * h * b * max_q) * part + 16 * (b * max_q * h + 64)
-    assert (n == 0) == (b == 1000 or (b, max_q) == (4, 2048) or (b == 128 and h == 16))
+    assert (n > 0) == (b == 1 and max_kv > 30000) or b != 1     # a few rows over a long context are split
     assert lib.m3_kv_attend_workspace_size(c, bt, h + 1 if kv > 1 else 0, 1, 1, 0) == 0
 
 

@@ -419,6 +419,21 @@ def test_attend(case, bound):
     bench.attend(q, n, io, causal, window, **tight)
 
 
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("batch,rows", [(300, 1), (40, 9), (2100, 1)])
+def test_attend_many_ragged_sequences(batch, rows, window):
+    """Lengths from nothing to many tiles dealt out among the workgroups: more sequences than threads, several row
+    tiles a sequence, idle slots between; and more sequences than a workgroup keeps account of."""
+    g = gen(batch)
+    top = 1300 if batch < 1000 else 1100
+    lens = torch.randint(0, 90 if batch > 1000 else top, (batch,), generator=g).tolist()
+    lens[3], lens[batch // 2], lens[-1], lens[1] = top, 0, 0, top
+    bench = Bench(batch, 1, 16, 16, top, I8, seed=batch)
+    bench.append(lens)
+    q = normal(g, batch * rows, 4, 16, dtype=F32)
+    bench.attend(q, [rows] * batch, F32, window=window)
+
+
 def test_attend_scale_and_peaks():
     """Large scores: one key takes all; a zero scale gives the mean."""
     for io in (BF, F32):
