@@ -61,13 +61,12 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
     const int D = a.D;
     // of a wave's 16 keys and 4 pieces (of 16 codes) of K: this lane's
-    const int key = lane >> 2;
-    auto kc = [&](int j) { return (lane & 3) + (64 * wave + NT * j) % DP / 16; };
+    const int key = lane & 15;  // (16 keys in turn: a group of 16 lanes writes 16 bank columns)
+    auto kc = [&](int j) { return (lane >> 4) + (64 * wave + NT * j) % DP / 16; };
 
     // this wave's rows
     u32x4 qf[QT][KM][NP];
     int klo[QT], khi[QT];
-    int w_lo = 0x7fffffff, w_hi = 0, all_lo = 0, all_hi = 0x7fffffff;
     const int wr0 = r0 + wave * 16 * QT;
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
@@ -84,20 +83,14 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         }
         khi[qt] = !live ? 0 : a.causal ? int(min(int64_t(held), base + tok + 1)) : held;
         klo[qt] = !live || !a.window ? 0 : int(max(base + tok - a.window + 1, int64_t(0)));
-        // keys that any and that every live row of the wave sees
-        int lo = live ? klo[qt] : 0x7fffffff, hi = khi[qt], alo = klo[qt], ahi = live ? khi[qt] : 0x7fffffff;
-#pragma unroll
-        for (int x = 1; x < 16; x <<= 1) {
-            lo = min(lo, __shfl_xor(lo, x));
-            hi = max(hi, __shfl_xor(hi, x));
-            alo = max(alo, __shfl_xor(alo, x));
-            ahi = min(ahi, __shfl_xor(ahi, x));
-        }
-        w_lo = min(w_lo, lo);
-        w_hi = max(w_hi, hi);
-        all_lo = max(all_lo, alo);
-        all_hi = min(all_hi, ahi);
     }
+    // keys that any and that every row of the wave sees (its rows follow one another)
+    const int wave_rows = min(16 * QT, rows - wr0);
+    const int64_t p0 = base + wr0 / a.group, p1 = base + (wr0 + wave_rows - 1) / a.group;
+    int w_lo = a.window ? int(max(p0 - a.window + 1, int64_t(0))) : 0;
+    int w_hi = wave_rows <= 0 ? 0 : a.causal ? int(max(min(int64_t(held), p1 + 1), int64_t(0))) : held;
+    int all_lo = a.window ? int(max(p1 - a.window + 1, int64_t(0))) : 0;
+    int all_hi = a.causal ? int(max(min(int64_t(held), p0 + 1), int64_t(0))) : held;
     w_lo = __builtin_amdgcn_readfirstlane(w_lo);
     w_hi = __builtin_amdgcn_readfirstlane(w_hi);
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
