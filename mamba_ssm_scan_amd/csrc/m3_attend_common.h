@@ -27,6 +27,9 @@ struct AttendDev {
     int splits;
     bool wide;
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
+    // of the tile kernel's launch:
+    int columns;     // (sequence, head, split)s side by side in an XCD (0: runs of workgroups)
+    int64_t grid;
 };
 
 hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s);

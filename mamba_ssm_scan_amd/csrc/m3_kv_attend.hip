@@ -509,7 +509,7 @@ hipError_t launch_attend(const AttendArgs& a) {
     AttendDev d{a.c, a.b, a.q, a.out, a.lse, reinterpret_cast<float*>(ws + p.o_off),
                 reinterpret_cast<float*>(ws + p.ml_off), reinterpret_cast<int*>(ws), p.items, a.q_heads,
                 a.q_heads / a.c.heads, a.c.headdim, __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows,
-                a.scale * kLog2e, a.causal, a.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks};
+                a.scale * kLog2e, a.causal, a.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks, 0, 0};
     if (p.tile) {
         const hipError_t e = launch_attend_tile(d, a.io, a.stream);
         return e != hipSuccess || p.splits == 1 ? e : launch_join<T>(d, a.stream);

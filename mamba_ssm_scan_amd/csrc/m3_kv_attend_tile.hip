@@ -36,12 +36,24 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int lr = lane & 15, g = lane >> 4;
-    // Workgroups go to the 8 XCDs in turn; each XCD gets a run of neighbours, which
-    // read the same keys of one (sequence, head, split) through its L2 at one time.
-    int64_t id = (blockIdx.x & 7) * int64_t(gridDim.x / 8) + (blockIdx.x >> 3);
-    if (id >= a.blocks) return;
-    const int64_t rt = a.row_tiles - 1 - id % a.row_tiles;  // causal: the longest first
-    id /= a.row_tiles;
+    // Workgroups go to the 8 XCDs in turn. A column is the row tiles of one (sequence,
+    // head, split), which read the same keys; each XCD takes whole columns, a.columns of
+    // them side by side, the last row tiles (with a causal mask the longest) of all first.
+    // Where that would leave XCDs idle (0), every XCD takes row tiles of all columns.
+    int64_t id, rt;
+    if (a.columns) {
+        const int x = blockIdx.x & 7, l = blockIdx.x >> 3;
+        const int mine = int((a.blocks / a.row_tiles - x + 7) / 8);  // columns of this XCD
+        const int at = l / int(a.columns * a.row_tiles), in = l % int(a.columns * a.row_tiles);
+        const int beside = min(a.columns, mine - at * a.columns);
+        if (beside <= 0 || in >= beside * a.row_tiles) return;
+        rt = a.row_tiles - 1 - in / beside;
+        id = (at * a.columns + in % beside) * int64_t(8) + x;
+    } else {
+        const int64_t all = a.blocks / a.row_tiles;
+        rt = a.row_tiles - 1 - blockIdx.x / all;
+        id = blockIdx.x % all;
+    }
     const int split = int(id % a.splits);
     id /= a.splits;
     const int H = a.c.heads, h = int(id % H);
@@ -268,39 +280,32 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
                 lv = 0.f;
             }
             u32x4 pf[QT][2][NV];
-            float add[QT], big = 0.f;
-            auto part = [&](int x, float c) {  // probability x % 16 of row tile x / 16
+            float c[QT], add[QT];
+            auto part = [&](int x) {  // probability x % 16 of row tile x / 16
                 const int qt = x / 16, j = x % 16;
-                return __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c));
+                return __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, c[qt]));
             };
-            auto close = [&](int qt, const float* p) {
-                add[qt] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) add[qt] += p[j];
-                pack_p<NV>(p, pf[qt]);
+            auto pair = [&](int x) {
+                const float lo = part(2 * x), hi = part(2 * x + 1);
+                add[x / 8] = x % 8 ? add[x / 8] + lo + hi : lo + hi;
+                pack_pair<NV>(lo, hi, pf[x / 8][x % 8 / 4], x % 4);
             };
-            {
-                float p[QT][16], c[QT];
+            constexpr int kSteps = 4 * KM, kPairs = 8 * QT;
 #pragma unroll
-                for (int qt = 0; qt < QT; ++qt) c[qt] = lv - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
-                constexpr int kSteps = 4 * KM;
+            for (int qt = 0; qt < QT; ++qt) c[qt] = lv - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
 #pragma unroll
-                for (int u = 0; u < kSteps; ++u) {
-                    if constexpr (kAhead) score_step(buf ^ 1, u / KM, u % KM, sn);
+            for (int u = 0; u < kSteps; ++u) {
+                if constexpr (kAhead) score_step(buf ^ 1, u / KM, u % KM, sn);
 #pragma unroll
-                    for (int x = u * 16 * QT / kSteps; x < (u + 1) * 16 * QT / kSteps; ++x) p[x / 16][x % 16] = part(x, c[x / 16]);
-                }
-#pragma unroll
-                for (int qt = 0; qt < QT; ++qt) {
-                    close(qt, p[qt]);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) big = fmaxf(big, p[qt][j]);
-                }
+                for (int x = u * kPairs / kSteps; x < (u + 1) * kPairs / kSteps; ++x) pair(x);
             }
+            bool big = false;
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) big |= !(add[qt] < kF16Top);
             // From 2^15 on, or before the first reference, the exact maximum is taken and all
             // of this tile's probabilities are formed again. (No short cut past `started`:
             // the arithmetic would move behind it, away from the products it runs beside.)
-            if (__any(int(!started) | int(big >= kF16Top))) {
+            if (__any(int(!started) | int(big))) {
                 started = true;
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
@@ -313,11 +318,9 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
                     sum[qt] *= fade;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
-                    const float c = lv - (m2 == -INFINITY ? 0.f : m2);
-                    float p[16];
+                    c[qt] = lv - (m2 == -INFINITY ? 0.f : m2);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = part(16 * qt + j, c);
-                    close(qt, p);
+                    for (int x = 0; x < 8; ++x) pair(8 * qt + x);
                     started = started && !__any(m2 == -INFINITY);
                 }
             }
@@ -383,8 +386,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 template <typename T, bool FP8, int DP, int QT, int NW>
 hipError_t launch_one(const AttendDev& d, hipStream_t s) {
     constexpr int kLds = 4 * 64 * DP * 2;
-    hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), dim3(unsigned((d.blocks + 7) / 8 * 8)), dim3(64 * NW),
-                       kLds, s, d);
+    hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), dim3(unsigned(d.grid)), dim3(64 * NW), kLds, s, d);
     return hipGetLastError();
 }
 // Rows a wave and waves (kTileRowsBf16 and kTileRowsF32 have their products): two tiles of 16 rows a wave
@@ -399,7 +401,18 @@ hipError_t launch_io(const AttendDev& d, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s) {
+hipError_t launch_attend_tile(const AttendDev& of, m3_dtype io, hipStream_t s) {
+    AttendDev d = of;
+    // Columns side by side: as many as leave their keys in an XCD's 4 MiB of L2. Whole
+    // columns where all XCDs get as many of them, or nearly so.
+    const int64_t columns = d.blocks / d.row_tiles, each = (columns + 7) / 8;
+    d.columns = 0;
+    d.grid = d.blocks;
+    if ((columns % 8 == 0 || columns >= 64) && 8 * each * d.row_tiles <= INT32_MAX) {
+        const int64_t fit = (int64_t(4) << 20) / (d.split_tiles * kTile * 2 * d.D);
+        d.columns = int(std::min(each, std::max<int64_t>(1, fit)));
+        d.grid = 8 * each * d.row_tiles;
+    }
     const bool fp8 = d.c.format == M3_KV_FP8;
     if (io == M3_BF16) return fp8 ? launch_io<bf16_t, true>(d, s) : launch_io<bf16_t, false>(d, s);
     return fp8 ? launch_io<float, true>(d, s) : launch_io<float, false>(d, s);
