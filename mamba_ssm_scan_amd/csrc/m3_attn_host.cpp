@@ -158,8 +158,12 @@ m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_hea
 
 namespace m3 {
 
-// Above 64 (row, head of a group) pairs a sequence, the kernel that shares each tile
-// of keys among 64 to 256 rows (m3_kv_attend_tile.hip); its keys are split, at least 8
+// Above 64 (row, head of a group) pairs a sequence (32 for fp32 rows and above headdim
+// 128, where the other kernel holds fewer rows a wave), the kernel that shares each tile
+// of keys among 64 to 256 rows (m3_kv_attend_tile.hip). 64 sequences of 4096 tokens, 8
+// heads, this kernel and the other: headdim 128, 64 pairs 249 and 172 us, 96 252 and 242,
+// 128 255 and 316; headdim 256, 32 pairs 311 and 343, 48 314 and 483; 16 of them in fp32,
+// headdim 128, 32 pairs 76 and 60, 64 80 and 89. Its keys are split, at least 8
 // tiles of 64 a workgroup, while there are fewer row tiles than two a CU. Else rows of
 // a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
 // twice the rows; at headdim above 128 the registers hold 16). A row tile and key head
@@ -174,8 +178,8 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     (void)causal;
     AttendPlan p{};
     const int64_t group = q_heads / c.heads, pairs = b.max_q * group;
-    p.tile = pairs > 64;
     const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
+    p.tile = pairs > (io == M3_BF16 && width < 2 ? 64 : 32);
     p.rows = p.tile ? (io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width] : pairs <= 16 || width == 2 ? 16 : 32;
     p.row_tiles = std::max<int64_t>(1, (pairs + p.rows - 1) / p.rows);
     int64_t tiles = (b.max_kv + 63) / 64;

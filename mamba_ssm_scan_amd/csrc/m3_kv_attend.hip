@@ -22,6 +22,12 @@
 //                 tokens of an entry, one 16-byte load
 // Each code is read from memory once per row tile, and the next tile's K and
 // page numbers are requested before this tile's softmax.
+//
+// Bound by memory, one read of the keys and values seen: 4 sequences of 131072 tokens
+// (4 heads of 128, e4m3) 99 us and 5 for the join, 5.4 TB/s; 128 sequences of 128 .. 4096
+// tokens (int8) 70 us, 3.9 TB/s, where 128 of 2112 each reach 5.1: the longest of a
+// workgroup's sequences decides. One sequence of 2048 is a chain of latencies (lengths,
+// page, codes, join): 8 and 5 us.
 #include <algorithm>
 
 #include "m3_attend_common.h"
@@ -131,269 +137,269 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
         zero_rows<T>(a, first_lds);
     }
     while (x < xe) {  // (a share may end one row tile's keys and begin the next's)
-    int64_t i, rt;
-    int h, t0 = 0, t1 = 0;
-    bool whole = true;
-    if constexpr (EVEN) {
-        int e = 0;
-        for (int hi = a.items - 1; e < hi;) {  // the last item that begins at or before x
-            const int mid = (e + hi + 1) / 2;
-            if (int64_t(H) * first_lds[mid] <= x) e = mid;
-            else hi = mid - 1;
-        }
-        const int n = first_lds[e + 1] - first_lds[e];
-        const int64_t off = x - int64_t(H) * first_lds[e];
-        h = int(off / n);
-        t0 = int(off - int64_t(h) * n);
-        t1 = int(min(int64_t(n), t0 + (xe - x)));
-        x += t1 - t0;
-        whole = t1 - t0 == n;
-        i = e / a.row_tiles;
-        rt = e % a.row_tiles;
-    } else {
-        x = xe;
-        rt = w % a.row_tiles;
-        const int64_t ih = w / a.row_tiles;
-        h = int(ih % H);
-        i = ih / H;
-    }
-    const Seq sq = seq_of(a.b, i);
-    const int rows = sq.n * a.group;
-    const int r0 = int(rt) * a.rows;
-    if (r0 >= rows) break;  // (without shares only)
-    const int64_t base = int64_t(sq.held) - sq.n;
-    const Span sp = span_of(a, sq, r0);
-    const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
-    if constexpr (EVEN) {
-        t0 += int(sp.lo);
-        t1 += int(sp.lo);
-    } else {
-        t0 = int(sp.lo);
-        t1 = int(sp.hi);
-    }
-    if (a.c.num_pages == 0) t1 = t0;
-
-    const int D = FULL ? DP : a.D;
-    const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
-    const int32_t* pages = a.b.pages + i * a.b.max_pages;
-    auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
-        if (blk >= held_blocks || (blk >> a.shift) >= a.b.max_pages) return -1;
-        const int64_t p = pages[blk >> a.shift];
-        if (p < 0 || p >= a.c.num_pages) return -1;
-        return ((int(p) * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
-    };
-    // Loads are unconditional (of block 0 where there is none, of piece 0 beyond
-    // headdim): a load behind a branch would wait for those before it. What they bring
-    // is masked below, or meets zeros of q.
-    const char* kbase = static_cast<const char*>(a.c.k) + (lr & 3) * D + (FULL ? 16 * g * KC : 0);
-    const char* vbase = static_cast<const char*>(a.c.v) + lr * 16;
-    u32x4 kr[4][KC];
-    auto load_k = [&](int kb) {
-        const char* p = kbase + uint64_t(unsigned(max(kb, 0))) * unsigned(16 * D);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int j = 0; j < KC; ++j) {
-                const int c = g * KC + j;
-                kr[t][j] = *reinterpret_cast<const u32x4*>(p + 4 * t * D + (FULL ? 16 * j : 16 * c < D ? 16 * c : 0));
+        int64_t i, rt;
+        int h, t0 = 0, t1 = 0;
+        bool whole = true;
+        if constexpr (EVEN) {
+            int e = 0;
+            for (int hi = a.items - 1; e < hi;) {  // the last item that begins at or before x
+                const int mid = (e + hi + 1) / 2;
+                if (int64_t(H) * first_lds[mid] <= x) e = mid;
+                else hi = mid - 1;
             }
-    };
-    int tile = t0 + wave;
-    int vb = -1;
-    if (tile < t1) {
-        vb = find(tile * 4 + g);
-        load_k(find(tile * 4 + (lr >> 2)));
-    }
-
-    // the rows' operands and the keys that each row sees
-    u32x4 qf[QT][2 * KC][NP];
-    int klo[QT], khi[QT];
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        const int r = r0 + 16 * qt + lr;
-        const bool live = r < rows;
-        const int tok = live ? r / a.group : 0, hq = h * a.group + (live ? r % a.group : 0);
-        const T* p = static_cast<const T*>(a.q.p) + (sq.row0 + tok) * a.q.token_stride + hq * a.q.head_stride;
-#pragma unroll
-        for (int m = 0; m < 2 * KC; ++m) {
-            const int d = 16 * (g * KC + m / 2) + 8 * (m & 1);
-#pragma unroll
-            for (int k = 0; k < NP; ++k) qf[qt][m][k] = u32x4{0, 0, 0, 0};
-            if (live && d < D) Parts<T>::load(p + d, a.wide, qf[qt][m]);
+            const int n = first_lds[e + 1] - first_lds[e];
+            const int64_t off = x - int64_t(H) * first_lds[e];
+            h = int(off / n);
+            t0 = int(off - int64_t(h) * n);
+            t1 = int(min(int64_t(n), t0 + (xe - x)));
+            x += t1 - t0;
+            whole = t1 - t0 == n;
+            i = e / a.row_tiles;
+            rt = e % a.row_tiles;
+        } else {
+            x = xe;
+            rt = w % a.row_tiles;
+            const int64_t ih = w / a.row_tiles;
+            h = int(ih % H);
+            i = ih / H;
         }
-        khi[qt] = !live ? 0 : a.causal ? int(min(int64_t(held), base + tok + 1)) : held;
-        klo[qt] = !live || !a.window ? 0 : int(max(base + tok - a.window + 1, int64_t(0)));
-    }
-    // keys that every row sees: tiles inside need no mask
-    const int rl = min(r0 + a.rows, rows) - 1;
-    const int all_hi = a.causal ? int(max(min(int64_t(held), base + r0 / a.group + 1), int64_t(0))) : held;
-    const int all_lo = a.window ? int(max(base + rl / a.group - a.window + 1, int64_t(0))) : 0;
-
-    floatx4 o[QT][DT];
-    float mx[QT], sum[QT];
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        mx[qt] = -INFINITY;
-        sum[qt] = 0.f;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
-    }
-    for (; tile < t1; tile += kWaves) {
-        u32x4 vr[DT];
-        {
-            const char* p = vbase + uint64_t(unsigned(max(vb, 0))) * unsigned(16 * D);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                vr[d] = *reinterpret_cast<const u32x4*>(p + (FULL || 16 * d < D ? 256 * d : 0));
+        const Seq sq = seq_of(a.b, i);
+        const int rows = sq.n * a.group;
+        const int r0 = int(rt) * a.rows;
+        if (r0 >= rows) break;  // (without shares only)
+        const int64_t base = int64_t(sq.held) - sq.n;
+        const Span sp = span_of(a, sq, r0);
+        const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
+        if constexpr (EVEN) {
+            t0 += int(sp.lo);
+            t1 += int(sp.lo);
+        } else {
+            t0 = int(sp.lo);
+            t1 = int(sp.hi);
         }
-        const bool there = vb >= 0;
-        float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
-        VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
-        const int k0 = tile * kTile, next = tile + kWaves;
-        int kb2 = -1, vb2 = -1;
-        if (next < t1) {
-            kb2 = find(next * 4 + (lr >> 2));
-            vb2 = find(next * 4 + g);
+        if (a.c.num_pages == 0) t1 = t0;
+
+        const int D = FULL ? DP : a.D;
+        const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
+        const int32_t* pages = a.b.pages + i * a.b.max_pages;
+        auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
+            if (blk >= held_blocks || (blk >> a.shift) >= a.b.max_pages) return -1;
+            const int64_t p = pages[blk >> a.shift];
+            if (p < 0 || p >= a.c.num_pages) return -1;
+            return ((int(p) * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
+        };
+        // Loads are unconditional (of block 0 where there is none, of piece 0 beyond
+        // headdim): a load behind a branch would wait for those before it. What they bring
+        // is masked below, or meets zeros of q.
+        const char* kbase = static_cast<const char*>(a.c.k) + (lr & 3) * D + (FULL ? 16 * g * KC : 0);
+        const char* vbase = static_cast<const char*>(a.c.v) + lr * 16;
+        u32x4 kr[4][KC];
+        auto load_k = [&](int kb) {
+            const char* p = kbase + uint64_t(unsigned(max(kb, 0))) * unsigned(16 * D);
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < KC; ++j) {
+                    const int c = g * KC + j;
+                    kr[t][j] = *reinterpret_cast<const u32x4*>(p + 4 * t * D + (FULL ? 16 * j : 16 * c < D ? 16 * c : 0));
+                }
+        };
+        int tile = t0 + wave;
+        int vb = -1;
+        if (tile < t1) {
+            vb = find(tile * 4 + g);
+            load_k(find(tile * 4 + (lr >> 2)));
         }
 
-        floatx4 s[QT][4];
+        // the rows' operands and the keys that each row sees
+        u32x4 qf[QT][2 * KC][NP];
+        int klo[QT], khi[QT];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int qt = 0; qt < QT; ++qt) {
+            const int r = r0 + 16 * qt + lr;
+            const bool live = r < rows;
+            const int tok = live ? r / a.group : 0, hq = h * a.group + (live ? r % a.group : 0);
+            const T* p = static_cast<const T*>(a.q.p) + (sq.row0 + tok) * a.q.token_stride + hq * a.q.head_stride;
 #pragma unroll
             for (int m = 0; m < 2 * KC; ++m) {
-                const u32x4 kf = to_bf16<FP8>(here(kr[t][m / 2][2 * (m & 1)]), here(kr[t][m / 2][2 * (m & 1) + 1]));
+                const int d = 16 * (g * KC + m / 2) + 8 * (m & 1);
 #pragma unroll
-                for (int qt = 0; qt < QT; ++qt) {
-                    if (m == 0) s[qt][t] = floatx4{0, 0, 0, 0};
-#pragma unroll
-                    for (int k = 0; k < NP; ++k) s[qt][t] = mfma(kf, qf[qt][m][k], s[qt][t]);
-                }
-                if (m % 4 == 3 || m == 2 * KC - 1) __builtin_amdgcn_sched_barrier(0);  // (conversions one after the other)
+                for (int k = 0; k < NP; ++k) qf[qt][m][k] = u32x4{0, 0, 0, 0};
+                if (live && d < D) Parts<T>::load(p + d, a.wide, qf[qt][m]);
             }
-        if (next < t1) load_k(kb2);
+            khi[qt] = !live ? 0 : a.causal ? int(min(int64_t(held), base + tok + 1)) : held;
+            klo[qt] = !live || !a.window ? 0 : int(max(base + tok - a.window + 1, int64_t(0)));
+        }
+        // keys that every row sees: tiles inside need no mask
+        const int rl = min(r0 + a.rows, rows) - 1;
+        const int all_hi = a.causal ? int(max(min(int64_t(held), base + r0 / a.group + 1), int64_t(0))) : held;
+        const int all_lo = a.window ? int(max(base + rl / a.group - a.window + 1, int64_t(0))) : 0;
 
-        // (a scale below 0 would turn the raw maximum round)
-        if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f))) {
+        floatx4 o[QT][DT];
+        float mx[QT], sum[QT];
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt)
+        for (int qt = 0; qt < QT; ++qt) {
+            mx[qt] = -INFINITY;
+            sum[qt] = 0.f;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int key = k0 + 16 * g + j;
-                    const float x = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
-                    s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? x : -INFINITY;
+            for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
+        }
+        for (; tile < t1; tile += kWaves) {
+            u32x4 vr[DT];
+            {
+                const char* p = vbase + uint64_t(unsigned(max(vb, 0))) * unsigned(16 * D);
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    vr[d] = *reinterpret_cast<const u32x4*>(p + (FULL || 16 * d < D ? 256 * d : 0));
+            }
+            const bool there = vb >= 0;
+            float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
+            VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
+            const int k0 = tile * kTile, next = tile + kWaves;
+            int kb2 = -1, vb2 = -1;
+            if (next < t1) {
+                kb2 = find(next * 4 + (lr >> 2));
+                vb2 = find(next * 4 + g);
+            }
+
+            floatx4 s[QT][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int m = 0; m < 2 * KC; ++m) {
+                    const u32x4 kf = to_bf16<FP8>(here(kr[t][m / 2][2 * (m & 1)]), here(kr[t][m / 2][2 * (m & 1) + 1]));
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt) {
+                        if (m == 0) s[qt][t] = floatx4{0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) s[qt][t] = mfma(kf, qf[qt][m][k], s[qt][t]);
+                    }
+                    if (m % 4 == 3 || m == 2 * KC - 1) __builtin_amdgcn_sched_barrier(0);  // (conversions one after the other)
                 }
-            ks = 1.f;
-            vs.log2 = 0.f;
-            // codes of slots that hold no token may be anything
-            const int nv = there ? min(max(held - (k0 + 16 * g), 0), 16) : 0;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int n = min(max(nv - 4 * w, 0), 4);
-                const unsigned keep = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) vr[d][w] &= keep;
-            }
-        }
-        float c[QT];
-        bool up = false;
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-            float top = s[qt][0][0];
-#pragma unroll
-            for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
-            c[qt] = quad_max(__builtin_fmaf(top, ks, vs.log2)) - kUp;
-            up |= c[qt] > mx[qt] + kSlack;
-        }
-        if (__any(up)) {
-#pragma unroll
-            for (int qt = 0; qt < QT; ++qt) {
-                const float m2 = fmaxf(mx[qt], c[qt]);
-                const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
-                mx[qt] = m2;
-                sum[qt] *= fade;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
-            }
-        }
-        u32x4 pf[QT][2][NV];
-#pragma unroll
-        for (int qt = 0; qt < QT; ++qt) {
-            const float off = vs.log2 - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
-            float add = 0.f;
-            float p[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, off));
-                add += p[j];
-            }
-            sum[qt] += add == 0.f ? 0.f : add * vs.inv;  // (a block no row sees may hold NaN)
-            pack_p<NV>(p, pf[qt]);
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const u32x4 vf = to_f16<FP8>(here(vr[d][2 * hf]), here(vr[d][2 * hf + 1]));
+            if (next < t1) load_k(kb2);
+
+            // (a scale below 0 would turn the raw maximum round)
+            if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f))) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                    for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
-                if (hf && d % 2) __builtin_amdgcn_sched_barrier(0);
+                    for (int j = 0; j < 16; ++j) {
+                        const int key = k0 + 16 * g + j;
+                        const float x = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
+                        s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? x : -INFINITY;
+                    }
+                ks = 1.f;
+                vs.log2 = 0.f;
+                // codes of slots that hold no token may be anything
+                const int nv = there ? min(max(held - (k0 + 16 * g), 0), 16) : 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int n = min(max(nv - 4 * w, 0), 4);
+                    const unsigned keep = n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) vr[d][w] &= keep;
+                }
             }
-        vb = vb2;
-    }
+            float c[QT];
+            bool up = false;
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+                float top = s[qt][0][0];
+#pragma unroll
+                for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
+                c[qt] = quad_max(__builtin_fmaf(top, ks, vs.log2)) - kUp;
+                up |= c[qt] > mx[qt] + kSlack;
+            }
+            if (__any(up)) {
+#pragma unroll
+                for (int qt = 0; qt < QT; ++qt) {
+                    const float m2 = fmaxf(mx[qt], c[qt]);
+                    const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
+                    mx[qt] = m2;
+                    sum[qt] *= fade;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
+                }
+            }
+            u32x4 pf[QT][2][NV];
+#pragma unroll
+            for (int qt = 0; qt < QT; ++qt) {
+                const float off = vs.log2 - (mx[qt] == -INFINITY ? 0.f : mx[qt]);
+                float add = 0.f;
+                float p[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, off));
+                    add += p[j];
+                }
+                sum[qt] += add == 0.f ? 0.f : add * vs.inv;  // (a block no row sees may hold NaN)
+                pack_p<NV>(p, pf[qt]);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const u32x4 vf = to_f16<FP8>(here(vr[d][2 * hf]), here(vr[d][2 * hf + 1]));
+#pragma unroll
+                    for (int qt = 0; qt < QT; ++qt)
+#pragma unroll
+                        for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
+                    if (hf && d % 2) __builtin_amdgcn_sched_barrier(0);
+                }
+            vb = vb2;
+        }
 
-    // the four waves' sums, brought to one maximum and added
+        // the four waves' sums, brought to one maximum and added
 #pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        sum[qt] = quad_sum(sum[qt]);
-        if (g == 0) {
-            m_lds[wave][16 * qt + lr] = mx[qt];
-            l_lds[wave][16 * qt + lr] = sum[qt];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int qt = 0; qt < QT; ++qt) {
-        float m = m_lds[0][16 * qt + lr];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, m_lds[w][16 * qt + lr]);
-        const float f = mx[qt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-            *reinterpret_cast<floatx4*>(&o_lds[wave][lr][16 * d + 4 * g]) = o[qt][d] * f;
-        __syncthreads();
-        const int per = D / 8;
-        for (int e = threadIdx.x; e < 16 * per; e += 64 * kWaves) {
-            const int q = e / per, d = 8 * (e - q * per);
-            const int r = r0 + 16 * qt + q;
-            if (16 * qt + q >= a.rows || r >= rows) continue;
-            float mm = m_lds[0][16 * qt + q];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, m_lds[w][16 * qt + q]);
-            float l = 0.f, v[8] = {};
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float mw = m_lds[w][16 * qt + q];
-                l += mw == -INFINITY ? l_lds[w][16 * qt + q] : l_lds[w][16 * qt + q] * __builtin_amdgcn_exp2f(mw - mm);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] += o_lds[w][q][d + k];
-            }
-            const int64_t at = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-            if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= inv;
-                store8<true>(static_cast<T*>(a.out) + at * D + d, v);
-                if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : mm * kLn2 + __logf(l);
-            } else {
-                const int64_t pt = int64_t(slot) * a.rows + 16 * qt + q;
-                store8<true>(a.part_o + pt * D + d, v);
-                if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pt) = float2{mm, l};
+        for (int qt = 0; qt < QT; ++qt) {
+            sum[qt] = quad_sum(sum[qt]);
+            if (g == 0) {
+                m_lds[wave][16 * qt + lr] = mx[qt];
+                l_lds[wave][16 * qt + lr] = sum[qt];
             }
         }
         __syncthreads();
-    }
+#pragma unroll
+        for (int qt = 0; qt < QT; ++qt) {
+            float m = m_lds[0][16 * qt + lr];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, m_lds[w][16 * qt + lr]);
+            const float f = mx[qt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                *reinterpret_cast<floatx4*>(&o_lds[wave][lr][16 * d + 4 * g]) = o[qt][d] * f;
+            __syncthreads();
+            const int per = D / 8;
+            for (int e = threadIdx.x; e < 16 * per; e += 64 * kWaves) {
+                const int q = e / per, d = 8 * (e - q * per);
+                const int r = r0 + 16 * qt + q;
+                if (16 * qt + q >= a.rows || r >= rows) continue;
+                float mm = m_lds[0][16 * qt + q];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, m_lds[w][16 * qt + q]);
+                float l = 0.f, v[8] = {};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    const float mw = m_lds[w][16 * qt + q];
+                    l += mw == -INFINITY ? l_lds[w][16 * qt + q] : l_lds[w][16 * qt + q] * __builtin_amdgcn_exp2f(mw - mm);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += o_lds[w][q][d + k];
+                }
+                const int64_t at = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
+                if (whole) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= inv;
+                    store8<true>(static_cast<T*>(a.out) + at * D + d, v);
+                    if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : mm * kLn2 + __logf(l);
+                } else {
+                    const int64_t pt = int64_t(slot) * a.rows + 16 * qt + q;
+                    store8<true>(a.part_o + pt * D + d, v);
+                    if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pt) = float2{mm, l};
+                }
+            }
+            __syncthreads();
+        }
     }
 }
 
