@@ -163,9 +163,15 @@ namespace m3 {
 // of keys among 64 to 256 rows (m3_kv_attend_tile.hip). 64 sequences of 4096 tokens, 8
 // heads, this kernel and the other: headdim 128, 64 pairs 249 and 172 us, 96 252 and 242,
 // 128 255 and 316; headdim 256, 32 pairs 311 and 343, 48 314 and 483; 16 of them in fp32,
-// headdim 128, 32 pairs 76 and 60, 64 80 and 89. Its keys are split, at least 8
-// tiles of 64 a workgroup, while there are fewer row tiles than two a CU. Else rows of
-// a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
+// headdim 128, 32 pairs 76 and 60, 64 80 and 89.
+//   A causal prompt whose workgroups would all run at once (two a CU up to headdim 64,
+// one above) ends with its last row tiles, so it takes half the rows a workgroup: one
+// prompt of 2048, 32 heads over 8, headdim 64 43 us and 51 with all rows, 128 67 and 81;
+// two of them 66 and 60, 127 and 98. A piece (fewer rows than half the keys) has row
+// tiles of nearly one length and keeps them whole (2048 of 32768: 574 us, 783 halved).
+//   Keys are split, at least 8 tiles of 64 a workgroup, while there are fewer workgroups
+// than CUs (one prompt of 2048, 16 heads over 2 of 128: 64 us, 76 up to two a CU).
+// Else rows of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
 // twice the rows; at headdim above 128 the registers hold 16). A row tile and key head
 // is a workgroup's where that fills the chip (two workgroups a CU, one above headdim
 // 128: 128 sequences of 2112 tokens, 4 heads, 54 us and 66 by even shares with their
@@ -175,12 +181,14 @@ namespace m3 {
 // not hurt.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
-    (void)causal;
     AttendPlan p{};
     const int64_t group = q_heads / c.heads, pairs = b.max_q * group;
     const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
     p.tile = pairs > (io == M3_BF16 && width < 2 ? 64 : 32);
     p.rows = p.tile ? (io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width] : pairs <= 16 || width == 2 ? 16 : 32;
+    if (p.tile && io == M3_BF16 && width < 2 && causal && 2 * b.max_q > b.max_kv &&
+        b.batch * c.heads * ((pairs + p.rows - 1) / p.rows) <= (width == 0 ? 512 : 256))
+        p.rows /= 2;
     p.row_tiles = std::max<int64_t>(1, (pairs + p.rows - 1) / p.rows);
     int64_t tiles = (b.max_kv + 63) / 64;
     if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);
@@ -191,7 +199,7 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     p.blocks = base;
     size_t parts = 0;  // rows of parts
     if (p.tile) {
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(512 / base, tiles / 8));
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / base, tiles / 8));
         p.split_tiles = (tiles + want - 1) / want;
         p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
         p.blocks = base * p.splits;

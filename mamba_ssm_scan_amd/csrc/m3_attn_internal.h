@@ -62,7 +62,8 @@ struct AttendPlan {
     size_t o_off, ml_off, total;  // workspace: the shares (even ones), sums of parts, (unit, sum) pairs
 };
 constexpr int32_t kAttendItems = 2048;  // most items whose first tiles a workgroup holds
-// Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256).
+// Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256);
+// bf16 rows up to headdim 128 also half of them.
 constexpr int32_t kTileRowsBf16[3] = {128, 256, 128}, kTileRowsF32[3] = {64, 128, 128};
 struct AttendArgs {
     m3_kv_cache c;

@@ -16,8 +16,8 @@
 // scaled and the tile's probabilities formed again. No maximum is needed otherwise: 16
 // probabilities, none negative, whose fp32 sum stays below 2^15 are below it themselves.
 //
-// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 570 us and 17 for the
-// join, 905 TFLOP/s; 4 prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s
+// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 571 us, 933 TFLOP/s; 4
+// prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s
 // of the pairs that the mask leaves. There the vector unit is the busiest (67%, the
 // products 25%): a score costs an exponential, a product and two sums whatever the
 // headdim, and at 64 there are half the products to hide them behind.
@@ -396,13 +396,17 @@ hipError_t launch_one(const AttendDev& d, hipStream_t s) {
     hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), dim3(unsigned(d.grid)), dim3(64 * NW), kLds, s, d);
     return hipGetLastError();
 }
-// Rows a wave and waves (kTileRowsBf16 and kTileRowsF32 have their products): two tiles of 16 rows a wave
-// where the registers hold them at two waves a SIMD.
+// Rows a wave and waves (the plan's rows are their products): two tiles of 16 rows a wave where the
+// registers hold them at two waves a SIMD, one where the plan halves the rows.
 template <typename T, bool FP8>
 hipError_t launch_io(const AttendDev& d, hipStream_t s) {
-    constexpr int kQt = sizeof(T) == 2 ? 2 : 1;
-    if (d.D <= 64) return launch_one<T, FP8, 64, kQt, 4>(d, s);
-    if (d.D <= 128) return launch_one<T, FP8, 128, kQt, 8>(d, s);
+    if constexpr (sizeof(T) == 2) {
+        if (d.D <= 64) return d.rows == 64 ? launch_one<T, FP8, 64, 1, 4>(d, s) : launch_one<T, FP8, 64, 2, 4>(d, s);
+        if (d.D <= 128) return d.rows == 128 ? launch_one<T, FP8, 128, 1, 8>(d, s) : launch_one<T, FP8, 128, 2, 8>(d, s);
+    } else {
+        if (d.D <= 64) return launch_one<T, FP8, 64, 1, 4>(d, s);
+        if (d.D <= 128) return launch_one<T, FP8, 128, 1, 8>(d, s);
+    }
     return launch_one<T, FP8, 256, 1, 8>(d, s);
 }
 

@@ -463,6 +463,12 @@ def test_attend_scores_that_jump(rows, dim, io):
     bench.attend(q, [rows] * 64, io, scale=1.0)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_scores_that_jump_in_prompts(dim):
+    """The same where the rows are most of the keys (half the rows a workgroup)."""
+    test_attend_scores_that_jump(150, dim, BF)
+
+
 def test_attend_missing_pages():
     """Keys of pages outside the pool are absent, at the start, inside, and all of a sequence's."""
     for n in ([1, 1, 1], [40, 130, 20]):
