@@ -15,7 +15,7 @@
 // that attention reads 16 tokens of an entry with one load). Other rows go through the
 // wave's own LDS rows in fp32. Waves never wait for each other after the angles.
 //
-// 4 prompts of 2048 (4 heads of 128 and 16 query heads, e4m3): 23 us, 4 TB/s of reads
+// 4 prompts of 2048 (4 heads of 128 and 16 query heads, e4m3): 25 us, 3.7 TB/s of reads
 // and writes (48 us with all rows through LDS); one token of each of 128 sequences: 5.7 us.
 // Reading a cache back: 9.0 us for the values of those prompts (25 MB), 7.8 us for the
 // last block of 128 sequences.

@@ -16,8 +16,8 @@
 // scaled and the tile's probabilities formed again. No maximum is needed otherwise: 16
 // probabilities, none negative, whose fp32 sum stays below 2^15 are below it themselves.
 //
-// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 571 us, 933 TFLOP/s; 4
-// prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s
+// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 557 us and 14 for the
+// join, 933 TFLOP/s; 4 prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s
 // of the pairs that the mask leaves. There the vector unit is the busiest (67%, the
 // products 25%): a score costs an exponential, a product and two sums whatever the
 // headdim, and at 64 there are half the products to hide them behind.
