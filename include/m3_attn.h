@@ -68,8 +68,9 @@ typedef struct m3_kv_cache {
  *          slot, whose rows are not stored and attend to nothing
  *   pages  [batch][max_pages]
  * max_q: at least the longest sequence's rows. max_kv: at least the largest
- * kv_len; rows beyond max_q and keys beyond max_kv are left out. Both only size
- * the launch: a bound that is too large costs little.
+ * kv_len. A sequence's rows beyond the first max_q are left out (not stored, their
+ * outputs not written) and keys beyond max_kv not seen; the other rows keep their
+ * positions. Both only size the launch: a bound that is too large costs little.
  */
 typedef struct m3_kv_batch {
     int64_t batch;

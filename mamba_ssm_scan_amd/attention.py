@@ -9,7 +9,7 @@ outputs and workspaces allocated with torch on the call's stream, no other imple
     q = cache.append(k, v, kv_len, pages, q=q, inv_freq=inv_freq)                # one new token a sequence
     o = cache.attend(q, kv_len, pages)
 
-A prompt, or a ragged batch, gives its row offsets `cu_q` and the longest `max_q`.
+A prompt, or a ragged batch, gives its row offsets `cu_q` and, if it is known, the longest `max_q`.
 """
 from __future__ import annotations
 
@@ -202,7 +202,8 @@ class KVCache:
     k_scale, v_scale [pages][heads][page_size / 16] fp32. Sequences, page tables and lengths are the caller's: `pages`
     [batch][max_pages] int32 names each sequence's pages in order, `kv_len` [batch] int32 its tokens with the call's
     new ones in (0: an idle slot). Rows of the call's tokens follow one another, `cu_q` [batch + 1] int32 where a
-    sequence may have other than one, `max_q` at least the longest.
+    sequence may have other than one, `max_q` at least the longest (all rows unless given, which sizes the launch for
+    one long sequence). Rows past `max_q` are left out, and what their outputs held stays.
     """
 
     def __init__(self, k, v, k_scale, v_scale):
@@ -244,10 +245,12 @@ class KVCache:
             cu = _dense(cu_q, "cu_q", dev, torch.int32, (b + 1,))
         elif tokens != b:
             raise ValueError(f"{tokens} rows for {b} sequences need cu_q")
+        if max_q is None:
+            max_q = 1 if cu is None else tokens
         return M3KvBatch(b, tokens, room, max_q, room * self.page_size if max_kv is None else max_kv, cu, lens, table)
 
     @_on_stream
-    def append(self, k, v, kv_len, pages, *, cu_q=None, max_q: int = 1, q=None, q_out=None, inv_freq=None,
+    def append(self, k, v, kv_len, pages, *, cu_q=None, max_q: Optional[int] = None, q=None, q_out=None, inv_freq=None,
                interleaved: bool = False, mscale: float = 1.0):
         """m3_kv_append: k, v [tokens][heads][dim] (bf16 or fp32) into the cache, the keys turned by inv_freq (None:
         as they are). With q [tokens][q_heads][dim], returns it turned by the same positions. stream: the current one
@@ -294,7 +297,7 @@ class KVCache:
         return k, v
 
     @_on_stream
-    def attend(self, q, kv_len, pages, *, cu_q=None, max_q: int = 1, max_kv: Optional[int] = None,
+    def attend(self, q, kv_len, pages, *, cu_q=None, max_q: Optional[int] = None, max_kv: Optional[int] = None,
                scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None, lse=False):
         """m3_kv_attend: q [tokens][q_heads][dim] over the cache; returns out, or (out, lse) with lse=True.
 

@@ -57,7 +57,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0) {
     const int r1 = min(r0 + a.rows, s.n * a.group) - 1;
-    const int64_t base = int64_t(s.held) - s.n;
+    const int64_t base = s.base;
     int64_t hi = min(int64_t(s.held), a.b.max_kv), lo = 0;
     if (a.causal) hi = min(hi, base + r1 / a.group + 1);
     if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);

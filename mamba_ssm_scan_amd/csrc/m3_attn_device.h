@@ -184,12 +184,13 @@ struct Code<false> {
     }
 };
 
-// Rows of a sequence of the batch, held inside [0, tokens) and [0, max_q]
-// whatever the device arrays hold.
+// Rows of a sequence of the batch, held inside [0, tokens) whatever the device arrays
+// hold. Rows beyond max_q are left out; those before them keep their positions.
 struct Seq {
     int64_t row0;  // its first row
-    int n;         // its rows
-    int held;      // tokens held once they are in (>= 0)
+    int n;         // its rows, max_q at most
+    int held;      // tokens held once all its rows are in (>= 0)
+    int base;      // position of its first row (negative: more rows than tokens held)
 };
 __device__ __forceinline__ Seq seq_of(const m3_kv_batch& b, int64_t i) {
     Seq s;
@@ -199,9 +200,11 @@ __device__ __forceinline__ Seq seq_of(const m3_kv_batch& b, int64_t i) {
         const int64_t hi = min(max(int64_t(b.cu_q[i + 1]), lo), b.tokens);
         s.row0 = lo;
         s.n = int(min(hi - lo, b.max_q));
+        s.base = s.held - int(hi - lo);
     } else {
         s.row0 = i;
         s.n = 1;
+        s.base = s.held - 1;
     }
     return s;
 }

@@ -330,11 +330,11 @@ __global__ __launch_bounds__(256, REG ? (N == 32 ? 4 : 2) : 1) void append_kerne
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int64_t i = blockIdx.x / a.nblk;
     const Seq q = seq_of(a.b, i);
-    const int64_t before = int64_t(q.held) - q.n;  // position of the sequence's first row (negative: not stored)
+    const int64_t before = q.base;  // position of the sequence's first row (negative: not stored)
     const int64_t blk = (before >> 4) + int(blockIdx.x % a.nblk);
     Where w;
     w.lo = int(max(before - 16 * blk, int64_t(0)));
-    w.hi = int(min(int64_t(q.held) - 16 * blk, int64_t(16)));
+    w.hi = int(min(before + q.n - 16 * blk, int64_t(16)));
     if (w.hi <= w.lo) return;  // (the workgroup as a whole)
     w.row = q.row0 + (16 * blk + w.lo - before);
     w.begun = w.lo > 0 && blk * 16 < before;

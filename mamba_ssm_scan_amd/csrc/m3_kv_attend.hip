@@ -167,7 +167,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
         const int rows = sq.n * a.group;
         const int r0 = int(rt) * a.rows;
         if (r0 >= rows) break;  // (without shares only)
-        const int64_t base = int64_t(sq.held) - sq.n;
+        const int64_t base = sq.base;
         const Span sp = span_of(a, sq, r0);
         const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
         if constexpr (EVEN) {

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     const int rows = sq.n * a.group;
     if (rt * a.rows >= rows) return;
     const int r0 = int(rt) * a.rows;
-    const int64_t base = int64_t(sq.held) - sq.n;
+    const int64_t base = sq.base;
     const Span sp = span_of(a, sq, r0);
     int t0 = int(sp.lo), t1 = int(sp.hi);
     if (a.splits > 1) {
