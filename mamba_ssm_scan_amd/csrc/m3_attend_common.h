@@ -116,8 +116,8 @@ struct Parts<float> {
 // denominator, in units of 2^(M - kUp). p' is at most 2^15 and is rounded to fp16 for
 // the product with V: 11 bits where bf16 would have 8, and what falls under fp16's
 // smallest number is below 2^-31 of the largest p'. fp32 rows add the rest of each p'
-// as a second fp16 part. The denominator takes p' in fp32 (its 1 / vs may differ
-// widely between blocks). A block whose scale is 0 holds zeros: it counts as 2^-60.
+// as a second fp16 part. The denominator takes p' in fp32, times 1 / vs of its block.
+// A block whose scale is 0 holds zeros: it counts as 2^-60.
 constexpr float kUp = 7.f, kSlack = 8.f;
 struct VScale {
     float log2, inv;
@@ -126,6 +126,19 @@ __device__ __forceinline__ VScale v_scale(float vs) {
     vs = vs == 0.f ? 8.673617379884035e-19f : vs;
     return VScale{__builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
 }
+// The denominator's unit. sum p' / vs is the softmax's sum in units of 2^M, but M follows
+// s + log2 vs: beside small scales the sum would leave fp32's range (keys of scale 2^-120
+// alone: 2^127 each). It is held in units of 2^(M - en), en a whole number per row: 0, or
+// M - n where M lies more than 2^64 below n, the largest score (log2, or the sum's own
+// log2); kept as g = 2^en, by which 1 / vs is multiplied. g is formed again for each tile
+// with a scale below 2^-85 or while a g of the wave is not 1: else a term stays below 2^100,
+// as p' does below 2^15. (Large scales need none: 2^-120 of a unit still has its 24 bits.)
+constexpr float kUnitSlack = 64.f, kSmallLog2 = -85.f;
+__device__ __forceinline__ float sum_unit(float d) {  // of d = M - n
+    const float e = d < -kUnitSlack && d > -1e30f ? fmaxf(__builtin_rintf(d), -120.f) : 0.f;
+    return __builtin_amdgcn_ldexpf(1.f, int(e));
+}
+__device__ __forceinline__ int unit_exp(float g) { return int(__float_as_uint(g) >> 23) - 127; }
 __device__ __forceinline__ unsigned pack_f16(float lo, float hi) {
     f16x2 v;
     v[0] = (_Float16)lo;  // nearest, ties to even

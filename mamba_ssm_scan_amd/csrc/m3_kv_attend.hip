@@ -122,6 +122,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
     constexpr int OS = DP + 4;         // LDS row of a wave's output
     __shared__ __align__(16) float o_lds[kWaves][16][OS];
     __shared__ float m_lds[kWaves][16 * QT], l_lds[kWaves][16 * QT];
+    __shared__ float g_lds[kWaves][16 * QT];
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int lr = lane & 15, g = lane >> 4;
@@ -236,11 +237,13 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
         const int all_lo = a.window ? int(max(base + rl / a.group - a.window + 1, int64_t(0))) : 0;
 
         floatx4 o[QT][DT];
-        float mx[QT], sum[QT];
+        float mx[QT], sum[QT], un[QT];
+        float small = kSmallLog2;  // scales below 2^small ask for the sums' units
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
             mx[qt] = -INFINITY;
             sum[qt] = 0.f;
+            un[qt] = 1.f;
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
         }
@@ -255,6 +258,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             const bool there = vb >= 0;
             float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
             VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
+            const float lv = vs.log2;
             const int k0 = tile * kTile, next = tile + kWaves;
             int kb2 = -1, vb2 = -1;
             if (next < t1) {
@@ -300,23 +304,35 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                     for (int d = 0; d < DT; ++d) vr[d][w] &= keep;
                 }
             }
-            float c[QT];
-            bool up = false;
+            float c[QT], top[QT];
+            bool up = lv < small;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
-                float top = s[qt][0][0];
+                top[qt] = s[qt][0][0];
 #pragma unroll
-                for (int j = 1; j < 16; ++j) top = fmaxf(top, s[qt][j / 4][j % 4]);
-                c[qt] = quad_max(__builtin_fmaf(top, ks, vs.log2)) - kUp;
+                for (int j = 1; j < 16; ++j) top[qt] = fmaxf(top[qt], s[qt][j / 4][j % 4]);
+                top[qt] = __builtin_fmaf(top[qt], ks, vs.log2);
+                c[qt] = quad_max(top[qt]) - kUp;
                 up |= c[qt] > mx[qt] + kSlack;
             }
             if (__any(up)) {
+                const bool units = __any(lv < small);
+                if (units) small = kSmallLog2;
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     const float m2 = fmaxf(mx[qt], c[qt]);
                     const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
+                    float fade_sum = fade;
+                    if (units) {
+                        const int e1 = unit_exp(un[qt]);
+                        const float n2 =
+                            fmaxf(quad_max(top[qt] - lv), mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
+                        un[qt] = sum_unit(m2 - n2);
+                        if (__any(un[qt] != 1.f)) small = INFINITY;
+                        if (m2 != -INFINITY) fade_sum = __builtin_amdgcn_exp2f(mx[qt] - m2 + float(unit_exp(un[qt]) - e1));
+                    }
                     mx[qt] = m2;
-                    sum[qt] *= fade;
+                    sum[qt] *= fade_sum;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
                 }
@@ -332,7 +348,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                     p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qt][j / 4][j % 4], ks, off));
                     add += p[j];
                 }
-                sum[qt] += add == 0.f ? 0.f : add * vs.inv;  // (a block no row sees may hold NaN)
+                sum[qt] += add == 0.f ? 0.f : add * (vs.inv * un[qt]);  // (a block no row sees may hold NaN)
                 pack_p<NV>(p, pf[qt]);
             }
 #pragma unroll
@@ -356,6 +372,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             if (g == 0) {
                 m_lds[wave][16 * qt + lr] = mx[qt];
                 l_lds[wave][16 * qt + lr] = sum[qt];
+                g_lds[wave][16 * qt + lr] = un[qt];
             }
         }
         __syncthreads();
@@ -378,18 +395,31 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
 #pragma unroll
                 for (int w = 1; w < kWaves; ++w) mm = fmaxf(mm, m_lds[w][16 * qt + q]);
                 float l = 0.f, v[8] = {};
+                int ee = 0;
+                bool far = false;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) far |= g_lds[w][16 * qt + q] != 1.f;
+                if (far) {  // a unit for the four sums
+                    float nn = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWaves; ++w)
+                        nn = fmaxf(nn, m_lds[w][16 * qt + q] - float(unit_exp(g_lds[w][16 * qt + q])) +
+                                           __builtin_amdgcn_logf(l_lds[w][16 * qt + q]));
+                    ee = unit_exp(sum_unit(mm - nn));
+                }
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w) {
-                    const float mw = m_lds[w][16 * qt + q];
-                    l += mw == -INFINITY ? l_lds[w][16 * qt + q] : l_lds[w][16 * qt + q] * __builtin_amdgcn_exp2f(mw - mm);
+                    const float mw = m_lds[w][16 * qt + q], lw = l_lds[w][16 * qt + q];
+                    l += mw == -INFINITY ? lw : lw * __builtin_amdgcn_exp2f(mw - mm + float(ee - unit_exp(g_lds[w][16 * qt + q])));
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] += o_lds[w][q][d + k];
                 }
                 const int64_t at = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-                if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] *= inv;
+                for (int k = 0; k < 8; ++k) v[k] = __builtin_amdgcn_ldexpf(v[k] * inv, ee);
+                mm -= float(ee);
+                if (whole) {
                     store8<true>(static_cast<T*>(a.out) + at * D + d, v);
                     if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : mm * kLn2 + __logf(l);
                 } else {

@@ -116,9 +116,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
     floatx4 o[QT][DT];
-    float mx[QT], sum[QT];
+    float mx[QT], sum[QT], un[QT];
 #pragma unroll
     for (int qt = 0; qt < QT; ++qt) {
+        un[qt] = 1.f;
         mx[qt] = wr0 + 16 * qt + lr < rows ? -INFINITY : 0.f;
         sum[qt] = 0.f;
 #pragma unroll
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         }
         __syncthreads();
     }
-    bool started = false;  // every row of the wave has a reference
+    float small = INFINITY;  // scales below 2^small ask for the maxima (all, until every row of the wave has a reference)
     auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4]) {
         fetch_v(tile + 1, pgv);  // (nothing after the last)
         if constexpr (kAhead) {
@@ -273,7 +274,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             if constexpr (!kAhead) scores(buf, s);
             const floatx4 sc = *reinterpret_cast<const floatx4*>(sc_lds[buf][g]);
             float ks = sc[0], lv = sc[1];
-            const float iv = sc[2];
+            const float lvs = sc[1], iv = sc[2];
             if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
@@ -309,30 +310,34 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             bool big = false;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) big |= !(add[qt] < kF16Top);
-            // From 2^15 on, or before the first reference, the exact maximum is taken and all
-            // of this tile's probabilities are formed again. (No short cut past `started`:
-            // the arithmetic would move behind it, away from the products it runs beside.)
-            if (__any(int(!started) | int(big))) {
-                started = true;
+            // From 2^15 on, before the first reference, or where a term could pass the sum's
+            // range, the exact maximum is taken and all of this tile's probabilities are
+            // formed again. (No short cut past `small`: the arithmetic would move behind it,
+            // away from the products it runs beside.)
+            if (__any(int(lvs < small) | int(big))) {
+                small = kSmallLog2;
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     float top = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < 16; ++j) top = fmaxf(top, __builtin_fmaf(s[qt][j / 4][j % 4], ks, lv));
                     const float m2 = fmaxf(mx[qt], quad_max(top) - kUp);
+                    const int e1 = unit_exp(un[qt]);
+                    const float n2 = fmaxf(quad_max(top - lvs), mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
+                    un[qt] = sum_unit(m2 - n2);
                     const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
+                    sum[qt] *= m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2 + float(unit_exp(un[qt]) - e1));
                     mx[qt] = m2;
-                    sum[qt] *= fade;
 #pragma unroll
                     for (int d = 0; d < DT; ++d) o[qt][d] *= fade;
                     c[qt] = lv - (m2 == -INFINITY ? 0.f : m2);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) pair(8 * qt + x);
-                    started = started && !__any(m2 == -INFINITY);
+                    small = __any(m2 == -INFINITY || un[qt] != 1.f) ? INFINITY : small;
                 }
             }
 #pragma unroll
-            for (int qt = 0; qt < QT; ++qt) sum[qt] += add[qt] == 0.f ? 0.f : add[qt] * iv;  // (a block no row sees may hold NaN)
+            for (int qt = 0; qt < QT; ++qt) sum[qt] += add[qt] == 0.f ? 0.f : add[qt] * (iv * un[qt]);  // (a block no row sees may hold NaN)
             const char* vi = lds + (2 + buf) * KB + lane * 16;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -366,12 +371,14 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         if (r >= rows) continue;
         const int64_t row = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
         const bool whole = a.splits == 1;
-        const float f = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l, unit = mx[qt] - float(unit_exp(un[qt]));
         const int64_t pt = whole ? row : split * a.b.tokens * a.q_heads + row;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             if (16 * d >= D) break;
-            const floatx4 v = o[qt][d] * f;
+            floatx4 v = o[qt][d] * f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = __builtin_amdgcn_ldexpf(v[k], unit_exp(un[qt]));
             const int64_t e = pt * D + 16 * d + 4 * g;
             if (!whole) {
                 *reinterpret_cast<floatx4*>(a.part_o + e) = v;
@@ -383,9 +390,9 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         }
         if (g == 0) {
             if (!whole)
-                *reinterpret_cast<float2*>(a.part_ml + 2 * pt) = float2{mx[qt], l};
+                *reinterpret_cast<float2*>(a.part_ml + 2 * pt) = float2{unit, l};
             else if (a.lse)
-                a.lse[row] = l == 0.f ? -INFINITY : mx[qt] * kLn2 + __logf(l);
+                a.lse[row] = l == 0.f ? -INFINITY : unit * kLn2 + __logf(l);
         }
     }
 }

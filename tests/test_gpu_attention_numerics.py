@@ -1,0 +1,69 @@
+"""Attention over the 8-bit cache where its arithmetic is hardest: values of any size, keys that take nearly all of the
+softmax, sums that cancel; against 64 bits, with bounds that scale with the values."""
+import math
+
+import pytest
+import torch
+
+from tests import attn_ref as ref
+from tests.test_gpu_attention import BF, DEV, F32, F8, I8, Bench, gen, normal, within
+
+pytestmark = pytest.mark.gpu
+
+
+def bound_of(out, mag, e, keys, v, pmax, io):
+    """How far an entry may be off. e: error of a score (a probability then moves by 4 e, the sum it is divided by
+    included). fp32 rows: 2^-23 of the output and of sum p |v|. bf16 rows: the output's rounding (8 significant bits:
+    2^-8), each probability's to fp16 (11 bits: 2^-11, or half of fp16's least step 2^-24 in a unit of which the
+    largest p * scale is at least 2^7: 2^-32 of the largest, times |code| <= |v| / scale, per key). 2^-133: bf16's
+    least number."""
+    r, rp = (2.0 ** -8, 2.0 ** -11) if io == BF else (2.0 ** -23, 2.0 ** -23)
+    least = keys * 2.0 ** -32 * pmax[..., None] * v.double().abs().max().item() if io == BF else 0.0
+    return r * out.abs() + mag * (rp * (1 + r) + 4 * e) + least + 2.0 ** -133
+
+
+def against_64_bits(bench, q, n, io, scale, score_roundings, cu=None):
+    """Outputs and lse of the cache's attention, each sequence's last n rows, against the values that it holds."""
+    out, lse = bench.cache.attend(q.to(DEV), bench.kv_len(), bench.pages, cu_q=cu, max_q=max(n), scale=scale, lse=True)
+    kd, vd = (x.cpu() for x in bench.held())
+    at = 0
+    for i, (c, L) in enumerate(zip(n, bench.len)):
+        k, v = kd[i, :L], vd[i, :L]
+        pos = torch.arange(L - c, L)
+        o, z, mag, top = ref.attend(q[at:at + c], pos, k, v, scale)
+        # sum p (over keys of values 1, the largest p in turn) is not needed to the bit: 1 bounds it
+        pmax = torch.ones_like(z)
+        e = 2.0 ** -24 * (L + score_roundings * top[..., None] + 8)
+        within(out[at:at + c], o, bound_of(o, mag, e, L, v, pmax, io), f"out {i}")
+        zb = e[..., 0] * 2 + z.abs() * 2.0 ** -22 + 1e-6
+        g = lse[at:at + c].cpu().double()
+        assert torch.isfinite(g).all() and ((g - z).abs() <= zb).all(), (i, (g - z).abs().max())
+        at += c
+    return out
+
+
+SIZES = {  # value magnitudes by token, in turn
+    "1e-33": [1e-33], "1e-35": [1e-35], "1e-33, 1": [1e-33, 1.0], "1, 1e-33": [1.0, 1e-33], "1e-30, 1e-33": [1e-30, 1e-33],
+    "1e-20, 1e-33, 1": [1e-20, 1e-33, 1.0], "1e35": [1e35], "1, 1e30": [1.0, 1e30], "1e25, 1e-10": [1e25, 1e-10],
+}
+
+
+@pytest.mark.parametrize("io", [BF], ids=["bf16"])
+@pytest.mark.parametrize("fmt,dim", [(I8, 64), (F8, 128), (I8, 256), (F8, 64)], ids=["int8-64", "e4m3-128", "int8-256", "e4m3-64"])
+@pytest.mark.parametrize("rows", [1, 70, 150])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_values_of_any_size(sizes, rows, fmt, dim, io):
+    """The softmax and its lse do not depend on how large the values are, and tiny values are not lost among themselves.
+    (Lengths that are split over workgroups and joined, and that are not.)"""
+    lens = [1100, 200, 33]
+    n = [min(rows, L) for L in lens]
+    bench = Bench(3, 1, dim, 16, max(lens), fmt, seed=dim + rows)
+    T = sum(lens)
+    pick = torch.cat([torch.arange(L) * len(SIZES[sizes]) // L for L in lens])
+    size = torch.tensor(SIZES[sizes], dtype=torch.float64)[pick][:, None, None]
+    k = normal(bench.g, T, 1, dim)
+    v = (normal(bench.g, T, 1, dim).double() * size).float()
+    bench.append(lens, rows=(k, v))
+    q = normal(bench.g, sum(n), 2, dim, dtype=io)
+    cu = None if n == [1, 1, 1] else torch.tensor([0, n[0], n[0] + n[1], sum(n)], dtype=torch.int32, device=DEV)
+    against_64_bits(bench, q, n, io, dim ** -0.5, dim + 4, cu)
