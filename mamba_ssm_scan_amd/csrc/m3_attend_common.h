@@ -117,14 +117,17 @@ struct Parts<float> {
 // the product with V: 11 bits where bf16 would have 8, and what falls under fp16's
 // smallest number is below 2^-31 of the largest p'. fp32 rows add the rest of each p'
 // as a second fp16 part. The denominator takes p' in fp32, times 1 / vs of its block.
-// A block whose scale is 0 holds zeros: it counts as 2^-60.
+// A block whose scale is 0 (or below the normal numbers) holds zeros, whatever its
+// codes: it counts as 2^-60.
 constexpr float kUp = 7.f, kSlack = 8.f;
 struct VScale {
     float log2, inv;
+    bool none;
 };
 __device__ __forceinline__ VScale v_scale(float vs) {
-    vs = vs == 0.f ? 8.673617379884035e-19f : vs;
-    return VScale{__builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs)};
+    const bool none = vs < 1.17549435e-38f;
+    vs = none ? 8.673617379884035e-19f : vs;
+    return VScale{__builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs), none};
 }
 // The denominator's unit. sum p' / vs is the softmax's sum in units of 2^M, but M follows
 // s + log2 vs: beside small scales the sum would leave fp32's range (keys of scale 2^-120

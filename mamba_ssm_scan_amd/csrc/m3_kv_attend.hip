@@ -283,7 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             if (next < t1) load_k(kb2);
 
             // (a scale below 0 would turn the raw maximum round)
-            if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f))) {
+            if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f) || vs.none)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                 ks = 1.f;
                 vs.log2 = 0.f;
                 // codes of slots that hold no token may be anything
-                const int nv = there ? min(max(held - (k0 + 16 * g), 0), 16) : 0;
+                const int nv = there && !vs.none ? min(max(held - (k0 + 16 * g), 0), 16) : 0;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int n = min(max(nv - 4 * w, 0), 4);

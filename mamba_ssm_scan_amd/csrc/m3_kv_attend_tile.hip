@@ -196,6 +196,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             const int p0 = 64 * swave + NT * j;
             const int blk = p0 / DP, d = p0 % DP + lane;
             u32x4 v = rv[j];
+            const VScale vs = v_scale(rvs[j]);
+            if (vs.none) v = u32x4{0, 0, 0, 0};
             if (tile * kTile + kTile > held) {  // codes of slots that hold no token may be anything
                 const int nv = min(max(held - (tile * kTile + 16 * blk), 0), 16);
 #pragma unroll
@@ -208,7 +210,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             *reinterpret_cast<u32x4*>(vp) = to_f16<FP8>(v[0], v[1]);
             *reinterpret_cast<u32x4*>(vp + 1024) = to_f16<FP8>(v[2], v[3]);
             if (p0 % DP == 0 && lane == 0) {
-                const VScale vs = v_scale(rvs[j]);
                 *reinterpret_cast<floatx4*>(sc_lds[buf][blk]) =
                     floatx4{rks[j] * a.scale2, vs.log2, vs.inv, there[j] ? 1.f : 0.f};
             }

@@ -67,3 +67,22 @@ def test_values_of_any_size(sizes, rows, fmt, dim, io):
     q = normal(bench.g, sum(n), 2, dim, dtype=io)
     cu = None if n == [1, 1, 1] else torch.tensor([0, n[0], n[0] + n[1], sum(n)], dtype=torch.int32, device=DEV)
     against_64_bits(bench, q, n, io, dim ** -0.5, dim + 4, cu)
+
+
+def test_a_scale_of_zero_holds_zeros_whatever_its_codes():
+    """Blocks whose scale is 0 (or below the normal numbers) are zeros, also where codes are not."""
+    for rows in (1, 70):
+        bench = Bench(1, 1, 64, 16, 200, I8, seed=rows)
+        bench.append([200])
+        p = int(bench.pages[0, 2])
+        bench.cache.v_scale[p] = 0.0
+        bench.cache.v_scale[int(bench.pages[0, 5])] = 1e-40
+        q = normal(bench.g, rows, 2, 64, dtype=F32)
+        cu = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+        out, lse = bench.cache.attend(q.to(DEV), bench.kv_len(), bench.pages, cu_q=cu, max_q=rows, lse=True)
+        kd, vd = (x[0].cpu() for x in bench.held())
+        vd[80:96] = 0
+        assert (vd[32:48] == 0).all()
+        o, z, mag, top = ref.attend(q, torch.arange(200 - rows, 200), kd, vd, 1 / 8)
+        within(out, o, ref.attend_bound(o, mag, top, 64, 200, F32), "out")
+        assert ((lse.cpu() - z).abs() <= 1e-4).all()
