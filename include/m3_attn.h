@@ -158,8 +158,10 @@ m3_status m3_kv_read(const m3_kv_cache* cache, int64_t batch, const int32_t* fir
  * q: rows of q_heads heads (a multiple of cache->heads). out [tokens][q_heads][headdim]
  * io dtype, dense, not overlapping an input; lse [tokens][q_heads] fp32 (natural
  * logarithm of the softmax's denominator), or NULL. Scores, the softmax and its
- * sums are fp32; with bf16 rows the probabilities are rounded to bf16 for the
- * product with V, with fp32 rows nothing is.
+ * sums are fp32. With fp32 rows nothing is rounded to fewer bits; with bf16 rows each
+ * probability is rounded to fp16 for the product with V: to 2^-11 of itself, or to 2^-32
+ * of the largest probability times V scale that the row sees, where that is more (keys
+ * more than about 14 nats below a key that takes all keep fewer bits).
  * workspace: at least m3_kv_attend_workspace_size() bytes, 16-byte aligned (NULL
  * when that is 0); holds the parts of rows whose keys are split over workgroups.
  */

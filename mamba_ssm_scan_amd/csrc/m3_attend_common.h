@@ -93,7 +93,7 @@ __device__ __forceinline__ void split3(float lo, float hi, unsigned* w) {
 template <>
 struct Parts<float> {
     static constexpr int kN = 3;
-    static constexpr int kV = 2;
+    static constexpr int kV = 3;
     __device__ __forceinline__ static void load(const float* p, bool wide, u32x4* f) {
         float v[8];
         if (wide)
@@ -113,10 +113,11 @@ struct Parts<float> {
 // Probabilities. p' = 2^(s + log2 vs - M + kUp): the score s (log2), the scale vs of
 // the key's V block, and the row's running reference M >= s + log2 vs - 8 of all keys
 // so far, so that sum p' code is the output's numerator and sum p' / vs its
-// denominator, in units of 2^(M - kUp). p' is at most 2^15 and is rounded to fp16 for
-// the product with V: 11 bits where bf16 would have 8, and what falls under fp16's
-// smallest number is below 2^-31 of the largest p'. fp32 rows add the rest of each p'
-// as a second fp16 part. The denominator takes p' in fp32, times 1 / vs of its block.
+// denominator, in units of 2^(M - kUp). p' is at most 2^15. For the product with V bf16
+// rows round it to fp16: 11 bits where bf16 would have 8, down to 2^-14 of the unit; below
+// it the last of the bits is 2^-24, that is 2^-31 of a largest p' of 2^7. fp32 rows split it
+// into three bf16 parts, which keep its 24 bits wherever it lies. The denominator takes p'
+// in fp32, times 1 / vs of its block.
 // A block whose scale is 0 (or below the normal numbers) holds zeros, whatever its
 // codes: it counts as 2^-60.
 constexpr float kUp = 7.f, kSlack = 8.f;
@@ -148,17 +149,17 @@ __device__ __forceinline__ unsigned pack_f16(float lo, float hi) {
     v[1] = (_Float16)hi;
     return __builtin_bit_cast(unsigned, v);
 }
-// Two probabilities as word w of the NV parts of a B operand, and 16 of them as the
-// operands of the two products with V's 16 tokens.
+// Two probabilities as word w of the NV parts of a B operand (one: fp16; three: bf16), and
+// 16 of them as the operands of the two products with V's 16 tokens.
 template <int NV>
 __device__ __forceinline__ void pack_pair(float lo, float hi, u32x4 (&f)[NV], int w) {
+    if constexpr (NV == 1) {
+        f[0][w] = pack_f16(lo, hi);
+    } else {
+        unsigned u[3];
+        split3(lo, hi, u);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const unsigned u = pack_f16(lo, hi);
-        f[k][w] = u;
-        const f16x2 r = __builtin_bit_cast(f16x2, u);
-        lo -= float(r[0]);
-        hi -= float(r[1]);
+        for (int k = 0; k < 3; ++k) f[k][w] = u[k];
     }
 }
 template <int NV>
@@ -177,7 +178,17 @@ __device__ __forceinline__ u32x4 to_bf16(unsigned a, unsigned b) {
     const u32x2 x = Code<FP8>::dec4_bf16(a), y = Code<FP8>::dec4_bf16(b);
     return u32x4{x[0], x[1], y[0], y[1]};
 }
-
+// V's codes as the probabilities' parts need them, and the product with one part
+template <bool FP8, int NV>
+__device__ __forceinline__ u32x4 v_operand(unsigned a, unsigned b) {
+    if constexpr (NV == 1) return to_f16<FP8>(a, b);
+    else return to_bf16<FP8>(a, b);
+}
+template <int NV>
+__device__ __forceinline__ floatx4 mfma_v(u32x4 v, u32x4 p, floatx4 c) {
+    if constexpr (NV == 1) return mfma_f16(v, p, c);
+    else return mfma(v, p, c);
+}
 
 // The larger of a lane's value and of the lanes 16 and 32 away (the four lanes
 // that share lane % 16), and their sum: register row swaps, no LDS round trip.

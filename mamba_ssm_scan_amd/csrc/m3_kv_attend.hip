@@ -3,11 +3,10 @@
 // o = sum_j p_j v_j with p the softmax of scale * q . k_j, in one pass over the
 // keys with a running reference and sum (log2 domain): when the reference grows,
 // what was summed is scaled down. The codes are exact in bf16 and fp16, so the
-// products run on MFMA over the codes themselves, q . k in bf16 and p . v in fp16,
-// with the block scales applied in fp32: K's to the scores, V's as log2 vs in the
-// probabilities' exponents (pack_p's comment). fp32 rows are split into three bf16
-// parts (24 bits) and their probabilities into two fp16 parts, so that nothing is
-// rounded to fewer bits.
+// products run on MFMA over the codes themselves, with the block scales applied in fp32:
+// K's to the scores, V's as log2 vs in the probabilities' exponents. bf16 rows take q . k
+// in bf16 and p . v in fp16 (p rounded to its 11 bits); fp32 rows and their probabilities
+// are split into three bf16 parts each (24 bits), so that nothing is rounded to fewer.
 //
 // attend_rows_kernel. A workgroup takes up to 16 QT rows of one (sequence, key
 // head) -- a row is a (token, head of the group) pair, so grouped heads share
@@ -355,11 +354,11 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const u32x4 vf = to_f16<FP8>(here(vr[d][2 * hf]), here(vr[d][2 * hf + 1]));
+                    const u32x4 vf = v_operand<FP8, NV>(here(vr[d][2 * hf]), here(vr[d][2 * hf + 1]));
 #pragma unroll
                     for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                        for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
+                        for (int k = 0; k < NV; ++k) o[qt][d] = mfma_v<NV>(vf, pf[qt][hf][k], o[qt][d]);
                     if (hf && d % 2) __builtin_amdgcn_sched_barrier(0);
                 }
             vb = vb2;

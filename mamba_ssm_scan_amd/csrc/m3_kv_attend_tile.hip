@@ -4,7 +4,8 @@
 // The products of m3_kv_attend.hip, S^T = K Q^T and O^T = V^T P^T with the scores
 // kept in registers, but bound by the matrix rate instead of by memory: a
 // workgroup of NW waves takes 16 QT NW rows, and its waves share each tile of 64
-// keys, which the workgroup turns from codes into bf16 (K) and fp16 (V) once and holds in LDS.
+// keys, which the workgroup turns from codes into bf16 (K; V of fp32 rows) or fp16 (V) once
+// and holds in LDS.
 // The LDS image is the operands themselves: a 1 KiB piece is the 64 lanes' 16
 // bytes of one MFMA operand, so every read is one linear ds_read_b128 that QT
 // products use. Two images alternate: the next tile's codes are on their way to
@@ -207,8 +208,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
                 }
             }
             char* vp = lds + (2 + buf) * KB + ((d / 16) * 2 * 64 + blk * 16 + d % 16) * 16;
-            *reinterpret_cast<u32x4*>(vp) = to_f16<FP8>(v[0], v[1]);
-            *reinterpret_cast<u32x4*>(vp + 1024) = to_f16<FP8>(v[2], v[3]);
+            *reinterpret_cast<u32x4*>(vp) = v_operand<FP8, NV>(v[0], v[1]);
+            *reinterpret_cast<u32x4*>(vp + 1024) = v_operand<FP8, NV>(v[2], v[3]);
             if (p0 % DP == 0 && lane == 0) {
                 *reinterpret_cast<floatx4*>(sc_lds[buf][blk]) =
                     floatx4{rks[j] * a.scale2, vs.log2, vs.inv, there[j] ? 1.f : 0.f};
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 #pragma unroll
                     for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
-                        for (int k = 0; k < NV; ++k) o[qt][d] = mfma_f16(vf, pf[qt][hf][k], o[qt][d]);
+                        for (int k = 0; k < NV; ++k) o[qt][d] = mfma_v<NV>(vf, pf[qt][hf][k], o[qt][d]);
                 }
         } else if (kAhead && seen(tile + 1)) {
             scores(buf ^ 1, sn);

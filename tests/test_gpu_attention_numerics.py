@@ -48,7 +48,7 @@ SIZES = {  # value magnitudes by token, in turn
 }
 
 
-@pytest.mark.parametrize("io", [BF], ids=["bf16"])
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("fmt,dim", [(I8, 64), (F8, 128), (I8, 256), (F8, 64)], ids=["int8-64", "e4m3-128", "int8-256", "e4m3-64"])
 @pytest.mark.parametrize("rows", [1, 70, 150])
 @pytest.mark.parametrize("sizes", SIZES)
@@ -86,3 +86,60 @@ def test_a_scale_of_zero_holds_zeros_whatever_its_codes():
         o, z, mag, top = ref.attend(q, torch.arange(200 - rows, 200), kd, vd, 1 / 8)
         within(out, o, ref.attend_bound(o, mag, top, 64, 200, F32), "out")
         assert ((lse.cpu() - z).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("io", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("nats", [0, 6, 10, 14, 18, 24, 40])
+@pytest.mark.parametrize("rows,dim,fmt", [(1, 64, I8), (20, 16, F8), (1, 256, F8), (70, 64, I8), (70, 128, F8), (70, 256, I8)])
+def test_a_sink_with_no_value(rows, dim, fmt, nats, io):
+    """The first key takes nearly all of the softmax and has no value: the output is the other keys', each of a small
+    probability. Scores come from one entry (a product without rounding), so that only the softmax is in question:
+    a score is rounded by the two scales, their product and the sum with the exponent (6 roundings)."""
+    L = 128
+    bench = Bench(1, 1, dim, 16, L, fmt, seed=dim + nats)
+    k, v = torch.zeros(L, 1, dim), normal(bench.g, L, 1, dim)
+    k[16:, 0, 0] = 0.5 * normal(bench.g, L - 16)
+    k[0, 0, 0] = nats
+    v[0] = 0.0
+    k[1:16] = 0.0
+    bench.append([L], rows=(k, v))
+    q = torch.zeros(rows, 2, dim, dtype=io)
+    q[..., 0] = 1.0
+    cu = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    against_64_bits(bench, q, [rows], io, 1.0, 6, cu)
+
+
+@pytest.mark.parametrize("dim,rows,fmt", [(64, 1, F8), (64, 3, I8), (128, 70, I8), (64, 70, F8), (256, 70, I8), (256, 2, F8)])
+def test_probabilities_of_bf16_rows_keep_11_bits(dim, rows, fmt):
+    """Values of both signs that cancel, a few keys: what is left shows the rounding of each probability."""
+    lens = [rows + 1 + j % 5 for j in range(48)]
+    bench = Bench(48, 1, dim, 16, max(lens), fmt, seed=dim + rows)
+    T = sum(lens)
+    v = torch.where(torch.arange(T) % 2 == 0, 1.0, -1.0)[:, None, None].expand(T, 1, dim).contiguous()
+    bench.append(lens, rows=(normal(bench.g, T, 1, dim), v))
+    n = [rows] * 48
+    q = normal(bench.g, sum(n), 4, dim, dtype=BF)
+    cu = torch.arange(0, 48 * rows + 1, rows, dtype=torch.int32, device=DEV)
+    against_64_bits(bench, q, n, BF, 2.0 * dim ** -0.5, dim + 4, cu)
+
+
+@pytest.mark.parametrize("lens,n", [([700, 300, 1500], [1, 1, 1]), ([900, 70, 400], [200, 70, 1]), ([2000, 40], [5, 5])], ids=str)
+def test_alone_or_in_a_batch(lens, n):
+    """A sequence alone and among others: the same values; their last bits may differ, as the keys may be cut elsewhere."""
+    H, D = 4, 128
+    bench = Bench(len(lens), 2, D, 64, max(lens), I8, seed=sum(lens))
+    bench.append(list(lens))
+    q = normal(bench.g, sum(n), H, D, dtype=F32).to(DEV)
+    cu = torch.tensor([sum(n[:j]) for j in range(len(n) + 1)], dtype=torch.int32, device=DEV)
+    whole = bench.cache.attend(q, bench.kv_len(), bench.pages, cu_q=cu, max_q=max(n))
+    kd, vd = (x.cpu() for x in bench.held())
+    at = 0
+    for i, c in enumerate(n):
+        one = bench.cache.attend(q[at:at + c], bench.kv_len()[i:i + 1], bench.pages[i:i + 1],
+                                 cu_q=torch.tensor([0, c], dtype=torch.int32, device=DEV), max_q=c)
+        o, _, mag, top = ref.attend(q[at:at + c].cpu(), torch.arange(lens[i] - c, lens[i]), kd[i, :lens[i]], vd[i, :lens[i]],
+                                    D ** -0.5)
+        bound = ref.attend_bound(o, mag, top, D, lens[i], F32)
+        within(whole[at:at + c], o, bound, f"among others {i}")
+        within(one, o, bound, f"alone {i}")
+        at += c
