@@ -137,7 +137,7 @@ __device__ __forceinline__ VScale v_scale(float vs) {
 // log2); kept as g = 2^en, by which 1 / vs is multiplied. g is formed again for each tile
 // with a scale below 2^-85 or while a g of the wave is not 1: else a term stays below 2^100,
 // as p' does below 2^15. (Large scales need none: 2^-120 of a unit still has its 24 bits.)
-constexpr float kUnitSlack = 64.f, kSmallLog2 = -85.f;
+constexpr float kUnitSlack = 64.f, kInvTop = 3.8685626e25f;  // 2^85
 __device__ __forceinline__ float sum_unit(float d) {  // of d = M - n
     const float e = d < -kUnitSlack && d > -1e30f ? fmaxf(__builtin_rintf(d), -120.f) : 0.f;
     return __builtin_amdgcn_ldexpf(1.f, int(e));

@@ -113,8 +113,15 @@ __device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) 
 // FULL: headdim is DP, so that every piece is there and loads have constant offsets.
 // EVEN: even shares (their bookkeeping takes registers that the other case keeps for
 // more waves).
+// Waves a SIMD: what the registers of each case allow without spilling in its loop.
+template <typename T, int DP, int QT, bool EVEN>
+constexpr int kSimdWaves = DP == 256 || (sizeof(T) == 4 && DP * QT > 128) ? 1
+                           : sizeof(T) == 4 || QT == 2                    ? 2
+                           : DP == 64                                     ? 4
+                           : EVEN                                         ? 2
+                                                                          : 3;
 template <typename T, bool FP8, int DP, int QT, bool FULL, bool EVEN>
-__global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * QT > 128) ? 1 : 2) void attend_rows_kernel(AttendDev a) {
+__global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void attend_rows_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KC = DP / 64;        // 16-code pieces of a key row a lane holds
     constexpr int DT = DP / 16;        // 16-entry tiles of the output
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
 
         floatx4 o[QT][DT];
         float mx[QT], sum[QT], un[QT];
-        float small = kSmallLog2;  // scales below 2^small ask for the sums' units
+        float inv_top = kInvTop;  // scales of a 1 / vs above it ask for the sums' units
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
             mx[qt] = -INFINITY;
@@ -257,7 +264,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
             const bool there = vb >= 0;
             float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
             VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
-            const float lv = vs.log2;
             const int k0 = tile * kTile, next = tile + kWaves;
             int kb2 = -1, vb2 = -1;
             if (next < t1) {
@@ -304,7 +310,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                 }
             }
             float c[QT], top[QT];
-            bool up = lv < small;
+            bool up = vs.inv > inv_top;
 #pragma unroll
             for (int qt = 0; qt < QT; ++qt) {
                 top[qt] = s[qt][0][0];
@@ -315,8 +321,8 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                 up |= c[qt] > mx[qt] + kSlack;
             }
             if (__any(up)) {
-                const bool units = __any(lv < small);
-                if (units) small = kSmallLog2;
+                const bool units = __any(vs.inv > inv_top);
+                if (units) inv_top = kInvTop;
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     const float m2 = fmaxf(mx[qt], c[qt]);
@@ -324,10 +330,10 @@ __global__ __launch_bounds__(64 * kWaves, DP == 256 || (sizeof(T) == 4 && DP * Q
                     float fade_sum = fade;
                     if (units) {
                         const int e1 = unit_exp(un[qt]);
-                        const float n2 =
-                            fmaxf(quad_max(top[qt] - lv), mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
+                        const float n2 = fmaxf(quad_max(top[qt] + __builtin_amdgcn_logf(vs.inv)),
+                                               mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
                         un[qt] = sum_unit(m2 - n2);
-                        if (__any(un[qt] != 1.f)) small = INFINITY;
+                        if (__any(un[qt] != 1.f)) inv_top = -INFINITY;
                         if (m2 != -INFINITY) fade_sum = __builtin_amdgcn_exp2f(mx[qt] - m2 + float(unit_exp(un[qt]) - e1));
                     }
                     mx[qt] = m2;

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     constexpr int NT = 64 * NW;
     constexpr int PC = 4 * DP / NT;      // 16-code pieces of K, and of V, a thread brings
     static_assert(PC >= 1 && 4 * DP % NT == 0, "threads and pieces");
-    constexpr bool kAhead = DP > 64;
+    constexpr bool kAhead = DP == 128;
     constexpr int KB = 64 * DP * 2;      // bytes of K's, and of V's, image
     extern __shared__ __align__(16) char lds[];  // two K images, two V images
     __shared__ float sc_lds[2][4][4];    // of the tile's blocks: K scale, log2 and inverse of V's, whether held
@@ -243,6 +243,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     // those with V beside the conversion of what comes next (K of n + 2, V of n + 1).
     // Headdim 64 has half the products for as many exponentials: there three waves a SIMD
     // without the second set of scores do better (K and V of n + 1 are converted in turn n).
+    // So do the two that headdim 256 leaves (one prompt of 2048, 16 heads over 4: bf16 103 us
+    // and 108 with the second set, fp32 164 and 203, where it spills).
     Pages pgv{}, pgk{};
     if (t0 < t1) {
         pgk = find(t0);
@@ -260,7 +262,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         }
         __syncthreads();
     }
-    float small = INFINITY;  // scales below 2^small ask for the maxima (all, until every row of the wave has a reference)
+    float inv_top = -INFINITY;  // scales of a 1 / vs above it ask for the maxima (all, until every row of the wave has a reference)
     auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4]) {
         fetch_v(tile + 1, pgv);  // (nothing after the last)
         if constexpr (kAhead) {
@@ -276,7 +278,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             if constexpr (!kAhead) scores(buf, s);
             const floatx4 sc = *reinterpret_cast<const floatx4*>(sc_lds[buf][g]);
             float ks = sc[0], lv = sc[1];
-            const float lvs = sc[1], iv = sc[2];
+            const float iv = sc[2];
             if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
@@ -314,10 +316,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             for (int qt = 0; qt < QT; ++qt) big |= !(add[qt] < kF16Top);
             // From 2^15 on, before the first reference, or where a term could pass the sum's
             // range, the exact maximum is taken and all of this tile's probabilities are
-            // formed again. (No short cut past `small`: the arithmetic would move behind it,
+            // formed again. (No short cut past `inv_top`: the arithmetic would move behind it,
             // away from the products it runs beside.)
-            if (__any(int(lvs < small) | int(big))) {
-                small = kSmallLog2;
+            if (__any(int(iv > inv_top) | int(big))) {
+                inv_top = kInvTop;
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt) {
                     float top = -INFINITY;
@@ -325,7 +327,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
                     for (int j = 0; j < 16; ++j) top = fmaxf(top, __builtin_fmaf(s[qt][j / 4][j % 4], ks, lv));
                     const float m2 = fmaxf(mx[qt], quad_max(top) - kUp);
                     const int e1 = unit_exp(un[qt]);
-                    const float n2 = fmaxf(quad_max(top - lvs), mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
+                    const float n2 = fmaxf(quad_max(top + __builtin_amdgcn_logf(iv)),
+                                           mx[qt] - float(e1) + __builtin_amdgcn_logf(quad_sum(sum[qt])));
                     un[qt] = sum_unit(m2 - n2);
                     const float fade = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2);
                     sum[qt] *= m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m2 + float(unit_exp(un[qt]) - e1));
@@ -335,7 +338,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
                     c[qt] = lv - (m2 == -INFINITY ? 0.f : m2);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) pair(8 * qt + x);
-                    small = __any(m2 == -INFINITY || un[qt] != 1.f) ? INFINITY : small;
+                    inv_top = __any(m2 == -INFINITY || un[qt] != 1.f) ? -INFINITY : inv_top;
                 }
             }
 #pragma unroll
