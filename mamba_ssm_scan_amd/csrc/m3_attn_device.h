@@ -60,6 +60,15 @@ __device__ __forceinline__ void cos_sin(int32_t pos, float f, double m, float* c
     *c = float(m * (((q + 1) & 2) ? -cc : cc));
 }
 
+// A launch of `blocks` workgroups (below 2^31): the first dimension holds fewer than 2^32
+// threads, so what is beyond 2^22 workgroups goes on along the third. The last may be
+// beyond `blocks`: every kernel returns where its index is.
+inline dim3 grid_of(int64_t blocks, unsigned y = 1) {
+    const int64_t x = int64_t(1) << 22;
+    return blocks <= x ? dim3(unsigned(blocks), y) : dim3(unsigned(x), y, unsigned((blocks + x - 1) / x));
+}
+__device__ __forceinline__ unsigned block_id() { return (blockIdx.z << 22) + blockIdx.x; }
+
 // One pair turned by (c, s). The products are rounded one by one (no fma): the
 // result is then the same wherever a pair is turned, and the codes that the
 // cache holds are those of the formula as written.

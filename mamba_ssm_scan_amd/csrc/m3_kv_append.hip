@@ -328,10 +328,12 @@ template <typename T, bool FP8, bool WIDE, int REG, int N>
 __global__ __launch_bounds__(256, REG ? (N == 32 ? 4 : 2) : 1) void append_kernel(AppendDev a) {
     extern __shared__ __align__(16) float lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int64_t i = blockIdx.x / a.nblk;
+    const unsigned id = block_id();
+    const int64_t i = id / unsigned(a.nblk);
+    if (i >= a.b.batch) return;
     const Seq q = seq_of(a.b, i);
     const int64_t before = q.base;  // position of the sequence's first row (negative: not stored)
-    const int64_t blk = (before >> 4) + int(blockIdx.x % a.nblk);
+    const int64_t blk = (before >> 4) + id % unsigned(a.nblk);
     Where w;
     w.lo = int(max(before - 16 * blk, int64_t(0)));
     w.hi = int(min(before + q.n - 16 * blk, int64_t(16)));
@@ -393,7 +395,7 @@ hipError_t launch_append(const AppendArgs& a) {
     d.k_slices = d.v_slices = slices(a.c.heads);
     const int y = 2 * d.k_slices + slices(d.q_heads);
     const size_t lds = size_t(waves) * 16 * a.c.headdim * 4 + (a.rot.inv_freq ? size_t(16) * d.half * 8 : 0);
-    const dim3 grid{unsigned(blocks), unsigned(y)}, block{unsigned(64 * waves)};
+    const dim3 grid = grid_of(blocks, unsigned(y)), block{unsigned(64 * waves)};
     auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, a.stream, d); };
     if (reg == 2)
         D <= 128 ? launch(append_kernel<T, FP8, true, 2, 32>) : launch(append_kernel<T, FP8, true, 2, 64>);
@@ -413,7 +415,7 @@ struct ReadDev {
     const int32_t* pages;
     void* k_out;
     void* v_out;
-    int64_t max_pages, max_count;
+    int64_t batch, max_pages, max_count;
     int D, shift, nblk;
 };
 
@@ -423,9 +425,11 @@ struct ReadDev {
 template <typename T, bool FP8>
 __global__ __launch_bounds__(256) void read_kernel(ReadDev a) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = blockIdx.x / a.nblk;
+    const unsigned id = block_id();
+    const int64_t i = id / unsigned(a.nblk);
+    if (i >= a.batch) return;
     const int64_t first = a.first[i], count = min(int64_t(max(a.count[i], 0)), a.max_count);
-    const int64_t blk = (first >> 4) + int(blockIdx.x % a.nblk);
+    const int64_t blk = (first >> 4) + id % unsigned(a.nblk);
     const int64_t j0 = 16 * blk - first;  // output row of slot 0
     const int H = a.c.heads, D = a.D;
     const int64_t at = block_at(a.pages + i * a.max_pages, a.max_pages, a.c.num_pages, a.shift, H, blk);
@@ -486,11 +490,11 @@ __global__ __launch_bounds__(256) void read_kernel(ReadDev a) {
 
 template <typename T, bool FP8>
 hipError_t launch_read(const ReadArgs& a) {
-    ReadDev d{a.c, a.first, a.count, a.pages, a.k_out, a.v_out, a.max_pages, a.max_count, a.c.headdim,
+    ReadDev d{a.c, a.first, a.count, a.pages, a.k_out, a.v_out, a.batch, a.max_pages, a.max_count, a.c.headdim,
               __builtin_ctz(unsigned(a.c.page_size / 16)), int((a.max_count + 14) / 16 + 1)};
     const int64_t blocks = a.batch * d.nblk;
     const int slices = int(std::max<int64_t>(1, std::min<int64_t>((2 * a.c.heads + 3) / 4, 2048 / blocks)));
-    const dim3 grid{unsigned(blocks), unsigned(slices)};
+    const dim3 grid = grid_of(blocks, unsigned(slices));
     hipLaunchKernelGGL((read_kernel<T, FP8>), grid, dim3(256), 0, a.stream, d);
     return hipGetLastError();
 }

@@ -135,7 +135,8 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
     const int H = a.c.heads;
     __shared__ int first_lds[EVEN ? kMaxItems + 1 : 1];
     __shared__ int scan_lds[kWaves];
-    const int w = blockIdx.x;
+    const int w = int(block_id());
+    if (w >= a.blocks) return;
     int64_t x = 0, xe = 1;  // what is left of this workgroup's share
     if constexpr (EVEN) {
         const int share = even_shares(a, first_lds, scan_lds);
@@ -445,7 +446,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
     __shared__ __align__(16) float o_lds[256 * 4];
     const int D = a.D, width = D <= 128 ? 32 : 64, crews = 256 / width;
     const int crew = threadIdx.x / width, lane = threadIdx.x % width, member = crew % team;
-    const int64_t at = int64_t(blockIdx.x) * (crews / team) + crew / team;
+    const int64_t at = int64_t(block_id()) * (crews / team) + crew / team;
     bool live = at < a.b.tokens * a.q_heads;
     const int64_t tok = live ? at / a.q_heads : 0;
     const int head = live ? int(at - tok * a.q_heads) : 0;
@@ -527,14 +528,14 @@ hipError_t launch_join(const AttendDev& d, hipStream_t s) {
     int team = 1;  // rows alone fill the chip from about 4 workgroups a CU
     while (team < crews && rows * team / crews < 1024) team *= 2;
     const int per = crews / team;
-    hipLaunchKernelGGL((attend_join_kernel<T>), dim3(unsigned((rows + per - 1) / per)), dim3(256), 0, s, d, team);
+    hipLaunchKernelGGL((attend_join_kernel<T>), grid_of((rows + per - 1) / per), dim3(256), 0, s, d, team);
     return hipGetLastError();
 }
 
 template <typename T, bool FP8, int DP, int QT>
 void launch_rows(const AttendDev& d, hipStream_t s) {
     auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(unsigned(d.blocks)), dim3(64 * kWaves), 0, s, d);
+        hipLaunchKernelGGL(kernel, grid_of(d.blocks), dim3(64 * kWaves), 0, s, d);
     };
     if (d.items)
         d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, true>)

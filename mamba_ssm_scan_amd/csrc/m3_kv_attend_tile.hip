@@ -48,9 +48,11 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     // head, split), which read the same keys; each XCD takes whole columns, a.columns of
     // them side by side, the last row tiles (with a causal mask the longest) of all first.
     // Where that would leave XCDs idle (0), every XCD takes row tiles of all columns.
+    const int wg = int(block_id());
+    if (wg >= a.grid) return;
     int64_t id, rt;
     if (a.columns) {
-        const int x = blockIdx.x & 7, l = blockIdx.x >> 3;
+        const int x = wg & 7, l = wg >> 3;
         const int mine = int((a.blocks / a.row_tiles - x + 7) / 8);  // columns of this XCD
         const int at = l / int(a.columns * a.row_tiles), in = l % int(a.columns * a.row_tiles);
         const int beside = min(a.columns, mine - at * a.columns);
@@ -59,8 +61,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         id = (at * a.columns + in % beside) * int64_t(8) + x;
     } else {
         const int64_t all = a.blocks / a.row_tiles;
-        rt = a.row_tiles - 1 - blockIdx.x / all;
-        id = blockIdx.x % all;
+        rt = a.row_tiles - 1 - wg / all;
+        id = wg % all;
     }
     const int split = int(id % a.splits);
     id /= a.splits;
@@ -405,7 +407,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 template <typename T, bool FP8, int DP, int QT, int NW>
 hipError_t launch_one(const AttendDev& d, hipStream_t s) {
     constexpr int kLds = 4 * 64 * DP * 2;
-    hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), dim3(unsigned(d.grid)), dim3(64 * NW), kLds, s, d);
+    hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), grid_of(d.grid), dim3(64 * NW), kLds, s, d);
     return hipGetLastError();
 }
 // Rows a wave and waves (the plan's rows are their products): two tiles of 16 rows a wave where the

@@ -47,7 +47,8 @@ __device__ __forceinline__ void angles(const RopeDev& a, int64_t t0, int nt, flo
 template <typename T, bool INTER>
 __global__ __launch_bounds__(kThreads) void rope_wide_kernel(RopeDev a) {
     __shared__ float2 cs[kMaxPairs];
-    const int64_t t0 = int64_t(blockIdx.x) * a.tb;
+    const int64_t t0 = int64_t(block_id()) * a.tb;
+    if (t0 >= a.tokens) return;
     const int nt = int(min(int64_t(a.tb), a.tokens - t0));
     angles(a, t0, nt, cs);
     const int turned = INTER ? a.half / 4 : a.half / 8;          // pieces (pairs of pieces) that turn
@@ -89,7 +90,8 @@ __global__ __launch_bounds__(kThreads) void rope_wide_kernel(RopeDev a) {
 template <typename T>
 __global__ __launch_bounds__(kThreads) void rope_any_kernel(RopeDev a) {
     __shared__ float2 cs[kMaxPairs];
-    const int64_t t0 = int64_t(blockIdx.x) * a.tb;
+    const int64_t t0 = int64_t(block_id()) * a.tb;
+    if (t0 >= a.tokens) return;
     const int nt = int(min(int64_t(a.tb), a.tokens - t0));
     const bool held = a.half <= kMaxPairs;
     if (held) angles(a, t0, nt, cs);
@@ -130,7 +132,7 @@ hipError_t launch(const RopeArgs& a) {
     int64_t tb = std::min<int64_t>((2 * kThreads * 16 + entries - 1) / entries, std::max(1, kMaxPairs / d.half));
     tb = std::max<int64_t>(1, std::min<int64_t>(tb, a.tokens / 1024));
     d.tb = int(tb);
-    const dim3 grid(unsigned((a.tokens + tb - 1) / tb));
+    const dim3 grid = grid_of((a.tokens + tb - 1) / tb);
     const bool inter = a.rot.interleaved != 0;
     if (a.wide && a.D % 8 == 0 && a.rot.rot % (inter ? 8 : 16) == 0 && d.half <= kMaxPairs) {
         if (inter)
