@@ -142,6 +142,9 @@ m3_kv_batch bounded(const m3_kv_batch& b, const m3_kv_cache& c) {
     return r;
 }
 
+// a window that no position reaches the end of, so that sums with it stay in range
+int64_t bounded(int64_t window) { return std::min(window, int64_t(1) << 31); }
+
 m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
     m3_status s;
@@ -350,7 +353,7 @@ size_t m3_kv_attend_workspace_size(const m3_kv_cache* cache, const m3_kv_batch* 
                                    m3_dtype io_dtype, int32_t causal, int64_t window) {
     clear_error();
     if (check_attend(cache, batch, q_heads, io_dtype, causal, window) != M3_OK) return 0;
-    return m3::attend_plan(*cache, bounded(*batch, *cache), q_heads, io_dtype, causal, window).total;
+    return m3::attend_plan(*cache, bounded(*batch, *cache), q_heads, io_dtype, causal, bounded(window)).total;
 }
 
 m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_rows* q, void* out, float* lse,
@@ -366,9 +369,9 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
     if (!aligned(out, 16)) return set_error(M3_EALIGN, "out is not 16-byte aligned");
     if (!aligned(lse, 4)) return set_error(M3_EALIGN, "lse is not 4-byte aligned");
     if (!std::isfinite(scale)) return set_error(M3_EINVAL, "scale is not finite");
-    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, causal ? 1 : 0, window,
-                     {}, workspace, wide_rows(*q, es), reinterpret_cast<hipStream_t>(stream)};
-    a.plan = m3::attend_plan(*cache, a.b, q_heads, io_dtype, causal, window);
+    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, causal ? 1 : 0,
+                     bounded(window), {}, workspace, wide_rows(*q, es), reinterpret_cast<hipStream_t>(stream)};
+    a.plan = m3::attend_plan(*cache, a.b, q_heads, io_dtype, causal, a.window);
     const size_t rows = size_t(T) * size_t(q_heads);
     const Range outs[] = {dense("out", out, rows * size_t(D) * es), dense("lse", lse, rows * 4),
                           dense("workspace", workspace, workspace_bytes)};
