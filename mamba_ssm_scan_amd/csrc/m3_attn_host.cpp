@@ -3,6 +3,7 @@
 // before the first HIP call.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "m3_attn_internal.h"
@@ -38,18 +39,33 @@ Range covered(const char* name, const m3_rows& r, int64_t tokens, int64_t heads,
     return Range{name, lo, lo + size_t((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + D) * es};
 }
 
-// Whether two sets of rows share bytes. Parts of one fused projection interleave:
-// with one token stride that holds each part's heads, their places within it decide.
+// Whether two sets of rows share bytes. Parts of one fused projection interleave: by token
+// (each part's heads together within a token stride; the common case, told by the parts'
+// places in it) or by head as well ([token][head][part][D]). Rows of the same strides share
+// bytes where some difference of their tokens and heads brings two of them closer than D.
 bool rows_overlap(const m3_rows& a, int64_t a_heads, const m3_rows& b, int64_t b_heads, int64_t tokens, int64_t D,
                   size_t es) {
     if (!overlaps(covered("", a, tokens, a_heads, D, es), covered("", b, tokens, b_heads, D, es))) return false;
-    const int64_t ea = (a_heads - 1) * a.head_stride + D, eb = (b_heads - 1) * b.head_stride + D;
-    if (tokens > 1 && (a.token_stride != b.token_stride || ea > a.token_stride || eb > b.token_stride)) return true;
-    if (tokens <= 1) return true;
-    const int64_t st = a.token_stride * int64_t(es);
-    int64_t off = (int64_t(reinterpret_cast<uintptr_t>(b.p)) - int64_t(reinterpret_cast<uintptr_t>(a.p))) % st;
-    if (off < 0) off += st;
-    return off < ea * int64_t(es) || off + eb * int64_t(es) > st;
+    const int64_t at = int64_t(reinterpret_cast<uintptr_t>(b.p)) - int64_t(reinterpret_cast<uintptr_t>(a.p));  // bytes
+    if (tokens > 1 && a.token_stride != b.token_stride) return true;  // (not told apart: taken to overlap)
+    const int64_t ts = a.token_stride * int64_t(es), row = D * int64_t(es);
+    const int64_t ea = (a_heads - 1) * a.head_stride * int64_t(es) + row, eb = (b_heads - 1) * b.head_stride * int64_t(es) + row;
+    if (tokens > 1 && ea <= ts && eb <= ts) {
+        int64_t off = at % ts;
+        if (off < 0) off += ts;
+        if (off >= ea && off + eb <= ts) return false;
+    }
+    if (a_heads > 1 && b_heads > 1 && a.head_stride != b.head_stride) return true;
+    const int64_t hs = (a_heads > 1 ? a : b).head_stride * int64_t(es);
+    for (int64_t h = 1 - b_heads; h < a_heads; ++h) {  // a's head less b's
+        const int64_t gap = at - h * hs;                // what the tokens' difference would have to make up
+        int64_t t = tokens > 1 && ts > 0 ? gap / ts : 0;
+        for (int64_t d = t - 1; d <= t + 1; ++d) {
+            const int64_t n = std::max(1 - tokens, std::min(tokens - 1, d));
+            if (std::abs(gap - n * ts) < row) return true;
+        }
+    }
+    return false;
 }
 
 constexpr int64_t kMaxStride = int64_t(1) << 31;  // times 2^30 tokens and 4 bytes: still within 64 bits

@@ -6,6 +6,7 @@ import sys
 
 import pytest
 
+from mamba_ssm_scan_amd import attention as at
 from tests.test_attn_abi import batch, cache, lib, place  # noqa: F401  (lib: the fixture)
 from tests.test_host_sanitizers import HERE, ROOT, _have_toolchain, host_check
 
@@ -23,6 +24,66 @@ def test_a_window_of_any_size(lib, max_q, tokens):
     for window in (1 << 17, (1 << 31) - 1, 1 << 31, (1 << 62) + 5, (1 << 63) - 64, (1 << 63) - 1):
         assert need(lib, b, 8, window=window) == want, window
     assert 0 < need(lib, b, 8, window=1 << 14) <= want
+
+
+def brute(pa, ta, ha, na, pb, tb, hb, nb, tokens, dim):
+    """Whether two sets of rows (bytes; strides in entries of 2 bytes) share a byte, entry by entry."""
+    seen = {pa + 2 * (t * ta + h * ha + d) for t in range(tokens) for h in range(na) for d in range(dim)}
+    return any(pb + 2 * (t * tb + h * hb + d) in seen for t in range(tokens) for h in range(nb) for d in range(dim))
+
+
+def test_overlaps_are_found_to_the_entry(lib):
+    """Rows of one buffer, interleaved by token and by head in every order: what shares an entry is refused. What
+    shares none is accepted by the overlap check; the call then ends at its next check (positions on the output)."""
+    import random
+    rng = random.Random(7)
+    told = {False: 0, True: 0}
+    for _ in range(4000):
+        tokens, heads, dim = rng.randint(1, 5), rng.randint(1, 4), rng.choice([2, 4, 6])
+        parts = rng.randint(2, 4)
+        if rng.random() < 0.5:   # [token][head][part][dim] with gaps
+            hs = parts * dim + rng.randint(0, 3)
+            ts = hs * heads + rng.randint(0, 5)
+        else:                    # [head][token][part][dim]
+            ts = parts * dim + rng.randint(0, 3)
+            hs = ts * tokens + rng.randint(0, 5)
+        shift = 2 * rng.randint(-3 * dim - ts, 3 * dim + ts)
+        base = place(7)
+        x, y = at.M3Rows(base + shift, ts, hs), at.M3Rows(base, ts, hs)
+        if shift == 0:
+            continue             # in place, which is allowed
+        rot = at.M3Rotary(place(6), 2, 0, 1.0)
+        s = lib.m3_rope(x, y, tokens, heads, dim, 1, base, rot, 0, None)
+        text = lib.m3_last_error().decode()
+        assert s == 1 and ("y overlaps x" in text or "y overlaps positions" in text), text
+        want = brute(base + shift, ts, hs, heads, base, ts, hs, heads, tokens, dim)
+        assert ("y overlaps x" in text) == want, (tokens, heads, dim, ts, hs, shift)
+        told[want] += 1
+    assert min(told.values()) > 300, told
+
+
+def test_overlaps_of_parts_of_different_head_counts(lib):
+    """q_out against k and v with other head counts: refused where an entry is shared; a call without an overlap ends
+    at the next check (q_out on kv_len)."""
+    import random
+    rng = random.Random(8)
+    told = {False: 0, True: 0}
+    for _ in range(3000):
+        tokens, g, q, dim = rng.randint(1, 4), rng.randint(1, 3), rng.randint(1, 6), 16
+        hs = rng.choice([1, 2, 3]) * dim + 2 * rng.randint(0, 2)
+        ts = hs * (q + 2 * g) + 2 * rng.randint(0, 3)
+        base = place(7)
+        off = 2 * rng.randint(-ts, ts + hs * g)
+        qr = at.M3Rows(base, ts, hs)
+        c = cache(heads=g, headdim=dim)
+        s = lib.m3_kv_append(c, batch(tokens=tokens, batch=tokens, kv_len=base), at.M3Rows(base + off, ts, hs),
+                             at.M3Rows(place(20), ts, hs), qr, qr, q, 1, None, None)
+        text = lib.m3_last_error().decode()
+        assert s == 1 and ("q_out overlaps k" in text), text
+        want = brute(base, ts, hs, q, base + off, ts, hs, g, tokens, dim)
+        assert (text == "q_out overlaps k") == want, (tokens, g, q, ts, hs, off, text)
+        told[want] += 1
+    assert min(told.values()) > 300, told
 
 
 def _toolchain():
