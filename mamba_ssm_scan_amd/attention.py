@@ -199,7 +199,7 @@ class KVCache:
     """A paged cache of keys and values in 8 bits, one scale per 16 tokens and head (the layout of m3_kv_cache).
 
     k [pages][heads][page_size / 16][16][dim] and v [pages][heads][page_size / 16][dim][16], int8 or float8_e4m3fn;
-    k_scale, v_scale [pages][heads][page_size / 16] fp32. Sequences, page tables and lengths are the caller's: `pages`
+    k_scale, v_scale [pages][heads][page_size / 16] fp32, kept for good: other tensors are another KVCache. Sequences, page tables and lengths are the caller's: `pages`
     [batch][max_pages] int32 names each sequence's pages in order, `kv_len` [batch] int32 its tokens with the call's
     new ones in (0: an idle slot). Rows of the call's tokens follow one another, `cu_q` [batch + 1] int32 where a
     sequence may have other than one, `max_q` at least the longest (all rows unless given, which sizes the launch for
@@ -217,7 +217,7 @@ class KVCache:
         _dense(v, "v", dev, k.dtype, (P, H, S, D, BLOCK))
         _dense(k_scale, "k_scale", dev, torch.float32, (P, H, S))
         _dense(v_scale, "v_scale", dev, torch.float32, (P, H, S))
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._k, self._v, self._k_scale, self._v_scale = k, v, k_scale, v_scale
         self.device, self.heads, self.head_dim, self.page_size = dev, H, D, S * BLOCK
         self._c = M3KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, S * BLOCK, H, D,
                             FORMATS[k.dtype])
@@ -233,6 +233,12 @@ class KVCache:
         scale = lambda: torch.empty((num_pages, heads, sub), dtype=torch.float32, device=device)  # noqa: E731
         return cls(new(num_pages, heads, sub, BLOCK, head_dim), new(num_pages, heads, sub, head_dim, BLOCK), scale(),
                    scale())
+
+    # calls go to the tensors that the cache was made of: their contents may change, the tensors not
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     def _batch(self, tokens, kv_len, pages, cu_q, max_q, max_kv) -> M3KvBatch:
         dev = self.device
