@@ -2,6 +2,7 @@
 
 torch tensors in, the C entry points of include/m3_attn.h called, as in `binding`: argument marshalling only,
 outputs and workspaces allocated with torch on the call's stream, no other implementation behind it.
+The cache's calls are for serving and take no part in autograd; `rope` does.
 
     cache = attention.KVCache.empty(num_pages, 64, kv_heads, head_dim)          # int8; or torch.float8_e4m3fn
     inv_freq, mscale = attention.rope_frequencies(head_dim)
@@ -175,13 +176,31 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[str] 
     return f.to(torch.float32).to(device), mscale
 
 
+class _Rope(torch.autograd.Function):
+    """rope as a step of autograd: linear, with the transposed map as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, positions, inv_freq, interleaved, mscale, backward):
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.how = dict(interleaved=interleaved, mscale=mscale, backward=not backward)
+        return rope(x.detach(), positions, inv_freq, interleaved=interleaved, mscale=mscale, backward=backward)
+
+    @staticmethod
+    def backward(ctx, dy):
+        dy = dy if dy.stride(-1) == 1 or dy.shape[-1] == 1 else dy.contiguous()
+        return rope(dy, *ctx.saved_tensors, **ctx.how), None, None, None, None, None
+
+
 @_on_stream
 def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1.0, backward: bool = False, out=None):
     """m3_rope: x [tokens][heads][dim] (bf16 or fp32) turned by positions [tokens] int32; returns out.
 
     backward: the transposed map (dL/dx from x = dL/dy). out may be x itself. stream: the current one unless given.
+    The result takes part in autograd where x does, unless out is given.
     """
     dev, dt = _device_of(x, "x"), x.dtype
+    if out is None and x.requires_grad and torch.is_grad_enabled():
+        return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward)
     code = binding._io_code(dt)
     rx = _rows(x, "x", dev, dt)
     shape = x.shape
@@ -199,11 +218,12 @@ class KVCache:
     """A paged cache of keys and values in 8 bits, one scale per 16 tokens and head (the layout of m3_kv_cache).
 
     k [pages][heads][page_size / 16][16][dim] and v [pages][heads][page_size / 16][dim][16], int8 or float8_e4m3fn;
-    k_scale, v_scale [pages][heads][page_size / 16] fp32, kept for good: other tensors are another KVCache. Sequences, page tables and lengths are the caller's: `pages`
-    [batch][max_pages] int32 names each sequence's pages in order, `kv_len` [batch] int32 its tokens with the call's
-    new ones in (0: an idle slot). Rows of the call's tokens follow one another, `cu_q` [batch + 1] int32 where a
-    sequence may have other than one, `max_q` at least the longest (all rows unless given, which sizes the launch for
-    one long sequence). Rows past `max_q` are left out, and what their outputs held stays.
+    k_scale, v_scale [pages][heads][page_size / 16] fp32; all kept for good (other tensors are another KVCache).
+    Sequences, page tables and lengths are the caller's: `pages` [batch][max_pages] int32 names each sequence's pages in
+    order, `kv_len` [batch] int32 its tokens with the call's new ones in (0: an idle slot). Rows of the call's tokens
+    follow one another, `cu_q` [batch + 1] int32 where a sequence may have other than one, `max_q` at least the longest
+    (all rows unless given, which sizes the launch for one long sequence). Rows past `max_q` are left out, and what
+    their outputs held stays.
     """
 
     def __init__(self, k, v, k_scale, v_scale):
