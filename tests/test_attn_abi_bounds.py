@@ -26,6 +26,22 @@ def test_a_window_of_any_size(lib, max_q, tokens):
     assert 0 < need(lib, b, 8, window=1 << 14) <= want
 
 
+@pytest.mark.parametrize("b,h,kv,max_q,max_kv,split", [
+    (1, 16, 4, 1, 131072, True),       # a few rows over a long context: even shares
+    (128, 16, 4, 1, 4096, False),      # 512 (sequence, head) pairs fill the chip by themselves
+    (3, 8, 8, 7, 1000, False),         # 16 tiles of keys: short
+    (3, 8, 8, 7, 1100, True),          # 18
+    (1, 4, 1, 512, 32768, True),       # a piece of a prompt in 8 workgroups: its keys are split
+    (4, 32, 8, 2048, 2048, False),     # prompts that fill the chip
+    (1000, 8, 8, 1, 64, False)])
+def test_workspace_where_keys_are_split_and_only_there(lib, b, h, kv, max_q, max_kv, split):
+    bt = batch(batch=b, tokens=b * max_q, max_q=max_q, max_kv=max_kv, cu_q=place(12), max_pages=-(-max_kv // 64))
+    n = need(lib, bt, h, kv=kv)
+    assert (n > 0) == split
+    # parts: headdim sums and two numbers each, at least two of the rows that a workgroup takes
+    assert not split or n >= 2 * 16 * (128 * 4 + 8)
+
+
 def brute(pa, ta, ha, na, pb, tb, hb, nb, tokens, dim):
     """Whether two sets of rows (bytes; strides in entries of 2 bytes) share a byte, entry by entry."""
     seen = {pa + 2 * (t * ta + h * ha + d) for t in range(tokens) for h in range(na) for d in range(dim)}
