@@ -70,7 +70,11 @@ typedef struct m3_kv_cache {
  * max_q: at least the longest sequence's rows. max_kv: at least the largest
  * kv_len. A sequence's rows beyond the first max_q are left out (not stored, their
  * outputs not written) and keys beyond max_kv not seen; the other rows keep their
- * positions. Both only size the launch: a bound that is too large costs little.
+ * positions. Both only size the launch. A max_kv that is too large costs a step or a
+ * piece of a prompt next to nothing; a prompt that starts a sequence may take a fifth
+ * longer (its rows are cut for the keys before it that the bound leaves room for).
+ * max_q also chooses the kernel for the whole batch: single tokens beside a long prompt
+ * run in tiles of many rows, so they are better off in a call of their own.
  */
 typedef struct m3_kv_batch {
     int64_t batch;

@@ -23,7 +23,7 @@ struct AttendDev {
     int q_heads, group, D, shift, rows;
     float scale2;    // scale * log2(e)
     int causal;
-    int64_t window, row_tiles, split_tiles;
+    int64_t window, row_tiles, split_tiles;  // split_tiles: of a split, as far as the bound tells
     int splits;
     bool wide;
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
@@ -63,6 +63,17 @@ __device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0
     if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);
     if (hi <= lo) return Span{0, 0};
     return Span{lo / kTile, (hi + kTile - 1) / kTile};
+}
+
+// How the kernel for many rows cuts a row tile's keys: into as many pieces as the plan has
+// workgroups for, from the keys that the tile sees (the plan knows a bound of them only),
+// at least kPieceTiles tiles each. One piece is written out directly, parts are joined.
+struct Cut {
+    int per, pieces;
+};
+__device__ __forceinline__ Cut cut_of(const AttendDev& a, const Span& sp) {
+    const int n = int(sp.hi - sp.lo), per = max((n + a.splits - 1) / a.splits, kPieceTiles);
+    return Cut{per, max((n + per - 1) / per, 1)};
 }
 
 // 8 entries of a query row as MFMA operands: one bf16 part, or three that add

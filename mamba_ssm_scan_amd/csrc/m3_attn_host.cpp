@@ -189,7 +189,11 @@ namespace m3 {
 // two of them 66 and 60, 127 and 98. A piece (fewer rows than half the keys) has row
 // tiles of nearly one length and keeps them whole (2048 of 32768: 574 us, 783 halved).
 //   Keys are split, at least 8 tiles of 64 a workgroup, while there are fewer workgroups
-// than CUs (one prompt of 2048, 16 heads over 2 of 128: 64 us, 76 up to two a CU).
+// than CUs (one prompt of 2048, 16 heads over 2 of 128: 64 us, 76 up to two a CU). The
+// splits come from the bound max_kv, their lengths from the keys that each row tile sees
+// (cut_of): 512 rows that end at 8192 under a bound of 131072 59.7 us, under their own 59.3
+// (294 with lengths from the bound). The halved rows need a tight bound: one prompt of 2048
+// under 4096 49 us at headdim 64 and 83 at 128, four of them under 131072 118 us and 108.
 // Else rows of a tile: 16 while a sequence has no more pairs, otherwise 32 (each key read once for
 // twice the rows; at headdim above 128 the registers hold 16). A row tile and key head
 // is a workgroup's where that fills the chip (two workgroups a CU, one above headdim
@@ -218,7 +222,7 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     p.blocks = base;
     size_t parts = 0;  // rows of parts
     if (p.tile) {
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / base, tiles / 8));
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / base, tiles / m3::kPieceTiles));
         p.split_tiles = (tiles + want - 1) / want;
         p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
         p.blocks = base * p.splits;

@@ -48,8 +48,8 @@ hipError_t launch_kv_read(const ReadArgs& a);
 
 // How the rows and keys of an attend call are cut: a tile of `rows` (row, head of
 // a group) pairs of one sequence and key head, its keys in tiles of 64. The kernel
-// for many rows: `splits` workgroups along a row tile's keys, `split_tiles` tiles
-// each. The kernel for few: `items` > 0 gives every workgroup an even share of all
+// for many rows: `splits` workgroups along a row tile's keys, at most `split_tiles`
+// tiles each (cut_of). The kernel for few: `items` > 0 gives every workgroup an even share of all
 // tiles, 0 a row tile each.
 struct AttendPlan {
     bool tile;            // the kernel for many rows a sequence
@@ -61,6 +61,7 @@ struct AttendPlan {
     int64_t blocks;       // workgroups
     size_t o_off, ml_off, total;  // workspace: the shares (even ones), sums of parts, (unit, sum) pairs
 };
+constexpr int32_t kPieceTiles = 8;      // least tiles of a piece, where a row tile's keys are cut (many rows)
 constexpr int32_t kAttendItems = 2048;  // most items whose first tiles a workgroup holds
 // Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256);
 // bf16 rows up to headdim 128 also half of them.

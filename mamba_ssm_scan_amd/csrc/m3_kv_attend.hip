@@ -479,7 +479,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
         step = 2 * a.rows;
     } else {
         const Span sp = live ? span_of(a, sq, r / a.rows * a.rows) : Span{0, 0};
-        parts = int((sp.hi - sp.lo + a.split_tiles - 1) / a.split_tiles);
+        parts = cut_of(a, sp).pieces;
+        live = live && parts > 1;
         p0 = p1 = at;
         step = a.b.tokens * a.q_heads;
     }

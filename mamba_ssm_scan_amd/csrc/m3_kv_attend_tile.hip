@@ -75,10 +75,13 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     const int64_t base = sq.base;
     const Span sp = span_of(a, sq, r0);
     int t0 = int(sp.lo), t1 = int(sp.hi);
+    bool whole = true;
     if (a.splits > 1) {
-        t0 = int(min(sp.lo + split * a.split_tiles, sp.hi));
-        t1 = int(min(sp.hi, t0 + a.split_tiles));
-        if (t0 >= t1) return;
+        const Cut cut = cut_of(a, sp);
+        if (split >= cut.pieces) return;
+        whole = cut.pieces == 1;
+        t0 += split * cut.per;
+        t1 = min(t1, t0 + cut.per);
     }
     const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
     const int D = a.D;
@@ -377,7 +380,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
         const int r = wr0 + 16 * qt + lr;
         if (r >= rows) continue;
         const int64_t row = (sq.row0 + r / a.group) * a.q_heads + h * a.group + r % a.group;
-        const bool whole = a.splits == 1;
         const float f = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l, unit = mx[qt] - float(unit_exp(un[qt]));
         const int64_t pt = whole ? row : split * a.b.tokens * a.q_heads + row;
 #pragma unroll
