@@ -180,14 +180,14 @@ namespace m3 {
 // Above 64 (row, head of a group) pairs a sequence (32 for fp32 rows and above headdim
 // 128, where the other kernel holds fewer rows a wave), the kernel that shares each tile
 // of keys among 64 to 256 rows (m3_kv_attend_tile.hip). 64 sequences of 4096 tokens, 8
-// heads, this kernel and the other: headdim 128, 64 pairs 249 and 172 us, 96 252 and 242,
-// 128 255 and 316; headdim 256, 32 pairs 311 and 343, 48 314 and 483; 16 of them in fp32,
-// headdim 128, 32 pairs 76 and 60, 64 80 and 89.
+// heads, that kernel and the one for few: headdim 128, 64 pairs 249 and 182 us, 96 252 and
+// 241, 128 255 and 328; headdim 256, 32 pairs 332 and 348, 48 335 and 487; 16 of them in
+// fp32, headdim 128, 32 pairs 77 and 65, 64 80 and 98.
 //   A causal prompt whose workgroups would all run at once (two a CU up to headdim 64,
 // one above) ends with its last row tiles, so it takes half the rows a workgroup: one
-// prompt of 2048, 32 heads over 8, headdim 64 43 us and 51 with all rows, 128 67 and 81;
+// prompt of 2048, 32 heads over 8, headdim 64 40 us and 49 with all rows, 128 68 and 83;
 // two of them 66 and 60, 127 and 98. A piece (fewer rows than half the keys) has row
-// tiles of nearly one length and keeps them whole (2048 of 32768: 574 us, 783 halved).
+// tiles of nearly one length and keeps them whole (2048 of 32768: 562 us, 783 halved).
 //   Keys are split, at least 8 tiles of 64 a workgroup, while there are fewer workgroups
 // than CUs (one prompt of 2048, 16 heads over 2 of 128: 64 us, 76 up to two a CU). The
 // splits come from the bound max_kv, their lengths from the keys that each row tile sees

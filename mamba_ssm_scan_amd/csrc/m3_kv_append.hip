@@ -15,9 +15,10 @@
 // that attention reads 16 tokens of an entry with one load). Other rows go through the
 // wave's own LDS rows in fp32. Waves never wait for each other after the angles.
 //
-// 4 prompts of 2048 (4 heads of 128 and 16 query heads, e4m3): 25 us, 3.7 TB/s of reads
-// and writes (48 us with all rows through LDS); one token of each of 128 sequences: 5.7 us.
-// Reading a cache back: 9.0 us for the values of those prompts (25 MB), 7.8 us for the
+// 4 prompts of 2048 (4 heads of 128 and 16 query heads, e4m3): 24 us, 3.8 TB/s of reads
+// and writes (31 us where half of each head turns in the half layout: too many registers as
+// pairs, so keys and queries go through LDS); one token of each of 128 sequences: 5.6 us.
+// Reading a cache back: 9.1 us for the values of those prompts (25 MB), 7.8 us for the
 // last block of 128 sequences.
 #include <algorithm>
 
@@ -388,7 +389,7 @@ hipError_t launch_append(const AppendArgs& a) {
     const int64_t blocks = a.b.batch * d.nblk;
     const int waves = a.c.headdim <= 128 ? 4 : 2;  // LDS rows and angles within 64 KiB
     // heads of a wave: 1, or as many as leave about 4 workgroups a CU, 8 of fp32 rows
-    // (4 prompts of 2048, 16 + 4 heads of 128: bf16 22.5 us and 23.8 with 8, fp32 42.6 with 4 and 39.1)
+    // (4 prompts of 2048, 16 + 4 heads of 128: bf16 24.0 us and 25.0 with 8, fp32 43.0 with 4 and 40.7)
     const int64_t wide = blocks * (2 * a.c.heads + d.q_heads);
     const int each = int(std::min<int64_t>(16, std::max<int64_t>(1, wide / (512 * int64_t(sizeof(T)) * waves))));
     auto slices = [&](int heads) { return (heads + waves * each - 1) / (waves * each); };

@@ -23,10 +23,12 @@
 // page numbers are requested before this tile's softmax.
 //
 // Bound by memory, one read of the keys and values seen: 4 sequences of 131072 tokens
-// (4 heads of 128, e4m3) 99 us and 5 for the join, 5.4 TB/s; 128 sequences of 128 .. 4096
+// (4 heads of 128, e4m3) 102 us with the join, 5.3 TB/s; 128 sequences of 128 .. 4096
 // tokens (int8) 70 us, 3.9 TB/s, where 128 of 2112 each reach 5.1: the longest of a
 // workgroup's sequences decides. One sequence of 2048 is a chain of latencies (lengths,
-// page, codes, join): 8 and 5 us.
+// page, codes, then the join's launch, as its 32 tiles are split over workgroups of four
+// waves): 8.5 and 4.5 us. 16 sequences of 8000 with 4 rows each (16 heads over 4 of 128): 36
+// us, of 64 of 2000 in fp32 (8 over 2) 29.
 #include <algorithm>
 
 #include "m3_attend_common.h"

@@ -17,11 +17,14 @@
 // scaled and the tile's probabilities formed again. No maximum is needed otherwise: 16
 // probabilities, none negative, whose fp32 sum stays below 2^15 are below it themselves.
 //
-// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 557 us and 14 for the
-// join, 933 TFLOP/s; 4 prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s
-// of the pairs that the mask leaves. There the vector unit is the busiest (67%, the
-// products 25%): a score costs an exponential, a product and two sums whatever the
-// headdim, and at 64 there are half the products to hide them behind.
+// 2048 rows after 30720 tokens (16 heads over 4 of 128, e4m3): 562 us with the join, 947
+// TFLOP/s; 4 prompts of 2048 (32 heads over 8 of 64, int8): 106 us, 650 TFLOP/s of the pairs
+// that the mask leaves. There the vector unit is the busiest (69%, the products 25%): 10.2
+// vector instructions are executed for each such score (7.9 in the other case), where the
+// softmax itself takes four: exponential, its argument, sum, rounding. The rest are the
+// conversions of codes, masks, and pairs that the mask drops; at 64 there are half the
+// products to hide them behind. fp32 rows take three products where bf16 rows take one: one
+// prompt of 2048, 16 heads over 4 of 64, 128, 256: 57, 103, 164 us (bf16, 256: 103).
 #include <algorithm>
 
 #include "m3_attend_common.h"
