@@ -373,29 +373,31 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
             vb = vb2;
         }
 
-        // the four waves' sums, brought to one maximum and added
+        // the four waves' sums, brought to one maximum and added (addresses from the thread's
+        // number anew: kept over the loop above they would cost it registers)
+        const int tid = int(here(threadIdx.x)), el = tid & 15, eg = (tid >> 4) & 3, ew = tid >> 6;
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
             sum[qt] = quad_sum(sum[qt]);
-            if (g == 0) {
-                m_lds[wave][16 * qt + lr] = mx[qt];
-                l_lds[wave][16 * qt + lr] = sum[qt];
-                g_lds[wave][16 * qt + lr] = un[qt];
+            if (eg == 0) {
+                m_lds[ew][16 * qt + el] = mx[qt];
+                l_lds[ew][16 * qt + el] = sum[qt];
+                g_lds[ew][16 * qt + el] = un[qt];
             }
         }
         __syncthreads();
 #pragma unroll
         for (int qt = 0; qt < QT; ++qt) {
-            float m = m_lds[0][16 * qt + lr];
+            float m = m_lds[0][16 * qt + el];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, m_lds[w][16 * qt + lr]);
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, m_lds[w][16 * qt + el]);
             const float f = mx[qt] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx[qt] - m);
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                *reinterpret_cast<floatx4*>(&o_lds[wave][lr][16 * d + 4 * g]) = o[qt][d] * f;
+                *reinterpret_cast<floatx4*>(&o_lds[ew][el][16 * d + 4 * eg]) = o[qt][d] * f;
             __syncthreads();
             const int per = D / 8;
-            for (int e = threadIdx.x; e < 16 * per; e += 64 * kWaves) {
+            for (int e = tid; e < 16 * per; e += 64 * kWaves) {
                 const int q = e / per, d = 8 * (e - q * per);
                 const int r = r0 + 16 * qt + q;
                 if (16 * qt + q >= a.rows || r >= rows) continue;
