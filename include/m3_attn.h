@@ -72,9 +72,9 @@ typedef struct m3_kv_cache {
  * outputs not written) and keys beyond max_kv not seen; the other rows keep their
  * positions. Both only size the launch. A max_kv that is too large costs a step or a
  * piece of a prompt next to nothing; a prompt that starts a sequence may take a fifth
- * longer (its rows are cut for the keys before it that the bound leaves room for).
- * max_q also chooses the kernel for the whole batch: single tokens beside a long prompt
- * run in tiles of many rows, so they are better off in a call of their own.
+ * longer (its row tiles are then as large as a piece's). A max_q of all rows costs up to a
+ * fifth. One kernel serves a batch, chosen by its rows: single tokens beside a long prompt
+ * may be better off in a call of their own.
  */
 typedef struct m3_kv_batch {
     int64_t batch;

@@ -20,6 +20,7 @@ struct AttendDev {
     float* part_ml;
     int* shares;     // even shares: tiles of a share, then the items' first tiles [items + 1]
     int items;       // (sequence, row tile) pairs; 0: no even shares
+    int packed;      // log2 of `rows` where the pairs follow one another (unit_of), else 0
     int q_heads, group, D, shift, rows;
     float scale2;    // scale * log2(e)
     int causal;
@@ -49,6 +50,15 @@ __device__ __forceinline__ floatx4 mfma_f16(u32x4 a, u32x4 b, floatx4 c) {
 __device__ __forceinline__ floatx4 mfma(u32x4 a, u32x4 b, floatx4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
+}
+
+// The sequence and row tile of pair e, and back.
+__device__ __forceinline__ Unit pair_of(const AttendDev& a, int e) {
+    if (a.packed) return unit_of(a.b, e, a.group, a.packed, 1);
+    return Unit{unsigned(e) / unsigned(a.row_tiles), unsigned(e) % unsigned(a.row_tiles)};
+}
+__device__ __forceinline__ int64_t pair_at(const AttendDev& a, int64_t i, int64_t rt) {
+    return a.packed ? first_unit(a.b, i, a.group, a.packed, 1) + rt : i * a.row_tiles + rt;
 }
 
 // Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see.

@@ -218,6 +218,28 @@ __device__ __forceinline__ Seq seq_of(const m3_kv_batch& b, int64_t i) {
     return s;
 }
 
+// Units of a ragged batch -- tiles of 2^shift (row, head of a group) pairs, or blocks of
+// tokens -- one after the other. Sequence i's begin at (cu_q[i] per >> shift) + extra i, which
+// leaves it the units of its rows (and of a first one begun before them, with extra 2), and
+// ends are found by a search of cu_q: a launch has work for nearly all its workgroups
+// however loose max_q is. `at`: the unit among its sequence's (negative or beyond its
+// rows: none; cu_q may be anything).
+__device__ __forceinline__ int64_t first_unit(const m3_kv_batch& b, int64_t i, int per, int shift, int extra) {
+    return (min(max(int64_t(b.cu_q[i]), int64_t(0)), b.tokens) * per >> shift) + extra * i;
+}
+struct Unit {
+    int64_t i, at;
+};
+__device__ __forceinline__ Unit unit_of(const m3_kv_batch& b, int64_t e, int per, int shift, int extra) {
+    int64_t lo = 0, hi = b.batch - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) / 2;
+        if (first_unit(b, mid, per, shift, extra) <= e) lo = mid;
+        else hi = mid - 1;
+    }
+    return Unit{lo, e - first_unit(b, lo, per, shift, extra)};
+}
+
 // Where block `blk` (16 tokens) of a sequence is held: its index among all
 // (page, head 0) blocks, or -1 where no page holds it. shift: log2(page_size / 16).
 __device__ __forceinline__ int64_t block_at(const int32_t* pages, int64_t max_pages, int64_t num_pages, int shift,

@@ -202,27 +202,41 @@ namespace m3 {
 // sequences of 701 tokens 15 and 26 us); else all tiles are dealt out in even shares
 // (64 sequences of 200 .. 8000 tokens: 68 us, 109 without), which a loose max_kv does
 // not hurt.
+//   max_q may be far above most sequences' rows. The kernel is chosen by four times the
+// mean where that is less, and the pairs are numbered one sequence's after the other's
+// (unit_of) instead of max_q's for each where that leaves out the half of them, or seven of
+// eight in the kernel for many rows, which then loses its order (longest tiles of all
+// sequences first, a column's in one XCD). Under a bound of all rows instead of the
+// longest's: 128 single tokens over 2100 57 us and 49 (187 by the bound alone), 64 prompts
+// of 300 113 and 100 (402), 4 prompts of 2048 108 and 107 (142 with the pairs packed).
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
                        int64_t window) {
     AttendPlan p{};
-    const int64_t group = q_heads / c.heads, pairs = b.max_q * group;
+    const int64_t group = q_heads / c.heads;
+    // what a sequence's rows are taken to be: the bound, or four times the mean below it
+    const int64_t mean = b.cu_q && b.batch > 0 ? (b.tokens + b.batch - 1) / b.batch : 1;
+    const int64_t most = std::min(b.max_q, 4 * mean), pairs = most * group;
+    auto each = [&](int64_t rows) { return std::max<int64_t>(1, (b.max_q * group + rows - 1) / rows); };
+    auto packed = [&](int64_t rows) { return b.tokens * group / rows + b.batch; };
     const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
     p.tile = pairs > (io == M3_BF16 && width < 2 ? 64 : 32);
     p.rows = p.tile ? (io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width] : pairs <= 16 || width == 2 ? 16 : 32;
-    if (p.tile && io == M3_BF16 && width < 2 && causal && 2 * b.max_q > b.max_kv &&
-        b.batch * c.heads * ((pairs + p.rows - 1) / p.rows) <= (width == 0 ? 512 : 256))
+    if (p.tile && io == M3_BF16 && width < 2 && causal && 2 * most > b.max_kv &&
+        c.heads * std::min(b.batch * each(p.rows), packed(p.rows)) <= (width == 0 ? 512 : 256))
         p.rows /= 2;
-    p.row_tiles = std::max<int64_t>(1, (pairs + p.rows - 1) / p.rows);
+    p.row_tiles = each(p.rows);
+    p.packed = b.cu_q && (p.tile ? 8 : 2) * packed(p.rows) <= b.batch * p.row_tiles;
     int64_t tiles = (b.max_kv + 63) / 64;
     if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);
     tiles = std::max<int64_t>(1, tiles);
-    const int64_t items = b.batch * p.row_tiles, base = std::max<int64_t>(1, items * c.heads);
+    const int64_t items = p.packed ? packed(p.rows) : b.batch * p.row_tiles, base = std::max<int64_t>(1, items * c.heads);
+    const int64_t busy = std::max<int64_t>(1, std::min(items, b.cu_q ? packed(p.rows) : items) * c.heads);
     p.splits = 1;
     p.split_tiles = tiles;
     p.blocks = base;
     size_t parts = 0;  // rows of parts
     if (p.tile) {
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / base, tiles / m3::kPieceTiles));
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / busy, tiles / m3::kPieceTiles));
         p.split_tiles = (tiles + want - 1) / want;
         p.splits = int32_t((tiles + p.split_tiles - 1) / p.split_tiles);
         p.blocks = base * p.splits;
@@ -328,7 +342,7 @@ m3_status m3_kv_append(const m3_kv_cache* cache, const m3_kv_batch* batch, const
                      q ? *q_out : m3_rows{nullptr, 0, 0}, q_heads, io_dtype,
                      rotary ? *rotary : m3_rotary{nullptr, 0, 0, 1.f}, wide, reinterpret_cast<hipStream_t>(stream)};
     if (T == 0 || batch->batch == 0 || a.b.max_q == 0) return M3_OK;
-    if (batch->batch * ((a.b.max_q + 14) / 16 + 1) > INT32_MAX)
+    if (m3::append_plan(a.b).blocks > INT32_MAX)
         return set_error(M3_EUNSUPPORTED, "batch times max_q / 16 is above 2^31");
     const hipError_t e = m3::launch_kv_append(a);
     if (e != hipSuccess) return set_error(M3_EHIP, "append launch failed: %s", hipGetErrorString(e));

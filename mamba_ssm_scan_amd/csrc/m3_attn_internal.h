@@ -33,6 +33,19 @@ struct AppendArgs {
 };
 hipError_t launch_kv_append(const AppendArgs& a);
 
+// Blocks of 16 tokens that an append launches workgroups for: every sequence's as many as
+// max_q rows may touch, or, where that is more than twice as many, one sequence's after
+// the other's (unit_of).
+struct AppendPlan {
+    int64_t each;    // blocks of a sequence; 0: one after the other
+    int64_t blocks;
+};
+inline AppendPlan append_plan(const m3_kv_batch& b) {
+    const int64_t each = (b.max_q + 14) / 16 + 1, packed = b.tokens / 16 + 2 * b.batch;
+    if (b.cu_q && 2 * packed <= b.batch * each) return AppendPlan{0, packed};
+    return AppendPlan{each, b.batch * each};
+}
+
 struct ReadArgs {
     m3_kv_cache c;
     int64_t batch, max_pages, max_count;
@@ -58,6 +71,7 @@ struct AttendPlan {
     int32_t splits;
     int64_t split_tiles;
     int32_t items;        // (sequence, row tile) pairs
+    bool packed;          // they follow one another (unit_of), as max_q is loose
     int64_t blocks;       // workgroups
     size_t o_off, ml_off, total;  // workspace: the shares (even ones), sums of parts, (unit, sum) pairs
 };

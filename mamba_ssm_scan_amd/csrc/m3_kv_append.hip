@@ -32,7 +32,7 @@ struct AppendDev {
     m3_kv_cache c;
     m3_kv_batch b;
     m3_rows k, v, q, qo;
-    int q_heads, D, half, interleaved, shift, nblk, k_slices, v_slices;
+    int q_heads, D, half, interleaved, shift, nblk, k_slices, v_slices;  // nblk 0: blocks one after the other (unit_of)
     int kq_jobs, v_jobs;      // register jobs of a row (0: the rows go through LDS)
     unsigned kq_inv, v_inv;   // ceil(2^16 / jobs): e / jobs = e * inv >> 16 for e < 512
     float mscale;
@@ -330,11 +330,12 @@ __global__ __launch_bounds__(256, REG ? (N == 32 ? 4 : 2) : 1) void append_kerne
     extern __shared__ __align__(16) float lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const unsigned id = block_id();
-    const int64_t i = id / unsigned(a.nblk);
-    if (i >= a.b.batch) return;
+    const Unit u = a.nblk ? Unit{id / unsigned(a.nblk), id % unsigned(a.nblk)} : unit_of(a.b, id, 1, 4, 2);
+    const int64_t i = u.i;
+    if (i >= a.b.batch || u.at < 0) return;
     const Seq q = seq_of(a.b, i);
     const int64_t before = q.base;  // position of the sequence's first row (negative: not stored)
-    const int64_t blk = (before >> 4) + id % unsigned(a.nblk);
+    const int64_t blk = (before >> 4) + u.at;
     Where w;
     w.lo = int(max(before - 16 * blk, int64_t(0)));
     w.hi = int(min(before + q.n - 16 * blk, int64_t(16)));
@@ -375,8 +376,9 @@ __global__ __launch_bounds__(256, REG ? (N == 32 ? 4 : 2) : 1) void append_kerne
 
 template <typename T, bool FP8>
 hipError_t launch_append(const AppendArgs& a) {
+    const AppendPlan plan = append_plan(a.b);
     AppendDev d{a.c, a.b, a.k, a.v, a.q, a.q_out, a.q.p ? a.q_heads : 0, a.c.headdim, a.rot.rot / 2,
-                a.rot.interleaved, __builtin_ctz(unsigned(a.c.page_size / 16)), int((a.b.max_q + 14) / 16 + 1),
+                a.rot.interleaved, __builtin_ctz(unsigned(a.c.page_size / 16)), int(plan.each),
                 0, 0, 0, 0, 0, 0, a.rot.mscale, a.rot.inv_freq};
     const int D = a.c.headdim, rot = a.rot.inv_freq ? a.rot.rot : 0;
     const bool pairs = rot && !a.rot.interleaved;
@@ -386,7 +388,7 @@ hipError_t launch_append(const AppendArgs& a) {
     d.v_jobs = D / 8;
     d.kq_inv = (65536u + d.kq_jobs - 1) / d.kq_jobs;
     d.v_inv = (65536u + d.v_jobs - 1) / d.v_jobs;
-    const int64_t blocks = a.b.batch * d.nblk;
+    const int64_t blocks = plan.blocks;
     const int waves = a.c.headdim <= 128 ? 4 : 2;  // LDS rows and angles within 64 KiB
     // heads of a wave: 1, or as many as leave about 4 workgroups a CU, 8 of fp32 rows
     // (4 prompts of 2048, 16 + 4 heads of 128: bf16 24.0 us and 25.0 with 8, fp32 43.0 with 4 and 40.7)

@@ -60,9 +60,10 @@ __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* 
     const int e0 = threadIdx.x * per, e1 = min(e0 + per, a.items);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
-        const Seq sq = seq_of(a.b, e / int(a.row_tiles));
-        const int r0 = e % int(a.row_tiles) * a.rows;
-        const Span sp = r0 < sq.n * a.group ? span_of(a, sq, r0) : Span{0, 0};
+        const Unit u = pair_of(a, e);
+        const Seq sq = seq_of(a.b, u.i);
+        const int64_t r0 = u.at * a.rows;
+        const Span sp = r0 >= 0 && r0 < sq.n * a.group ? span_of(a, sq, int(r0)) : Span{0, 0};
         first[e] = int(sp.hi - sp.lo);
         sum += int(sp.hi - sp.lo);
     }
@@ -100,8 +101,10 @@ template <typename T>
 __device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) {
     for (int e = blockIdx.x; e < a.items; e += int(a.blocks)) {
         if (first[e + 1] != first[e]) continue;
-        const Seq sq = seq_of(a.b, e / int(a.row_tiles));
-        const int r0 = e % int(a.row_tiles) * a.rows, r1 = min(r0 + a.rows, sq.n * a.group);
+        const Unit u = pair_of(a, e);
+        const Seq sq = seq_of(a.b, u.i);
+        if (u.at < 0 || u.at * a.rows >= sq.n * a.group) continue;
+        const int r0 = int(u.at) * a.rows, r1 = min(r0 + a.rows, sq.n * a.group);
         const int D = a.D, H = a.c.heads;
         for (int64_t k = threadIdx.x; k < int64_t(r1 - r0) * H * D; k += 64 * kWaves) {
             const int d = int(k % D), h = int(k / D % H), r = r0 + int(k / D / H);
@@ -157,15 +160,24 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
                 if (int64_t(H) * first_lds[mid] <= x) e = mid;
                 else hi = mid - 1;
             }
-            const int n = first_lds[e + 1] - first_lds[e];
-            const int64_t off = x - int64_t(H) * first_lds[e];
+            e = __builtin_amdgcn_readfirstlane(e);  // (the workgroup's: in scalars)
+            const int f0 = __builtin_amdgcn_readfirstlane(first_lds[e]);
+            const int n = __builtin_amdgcn_readfirstlane(first_lds[e + 1]) - f0;
+            const int64_t off = x - int64_t(H) * f0;
             h = int(off / n);
             t0 = int(off - int64_t(h) * n);
             t1 = int(min(int64_t(n), t0 + (xe - x)));
             x += t1 - t0;
             whole = t1 - t0 == n;
-            i = e / a.row_tiles;
-            rt = e % a.row_tiles;
+            const Unit u = pair_of(a, e);
+            i = u.i;
+            rt = u.at;
+        } else if (a.packed) {
+            x = xe;
+            const Unit u = pair_of(a, w / H);
+            h = w % H;
+            i = u.i;
+            rt = u.at;
         } else {
             x = xe;
             rt = w % a.row_tiles;
@@ -175,8 +187,8 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
         }
         const Seq sq = seq_of(a.b, i);
         const int rows = sq.n * a.group;
+        if (rt < 0 || rt * a.rows >= rows) break;  // (without shares only)
         const int r0 = int(rt) * a.rows;
-        if (r0 >= rows) break;  // (without shares only)
         const int64_t base = sq.base;
         const Span sp = span_of(a, sq, r0);
         const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
@@ -472,7 +484,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
     int64_t p0, p1, step;
     int parts;
     if (a.items) {
-        const int e = int(i * a.row_tiles) + r / a.rows, rin = r % a.rows;
+        const int e = live ? int(pair_at(a, i, r / a.rows)) : 0, rin = r % a.rows;
         const int share = a.shares[0], f = live ? a.shares[1 + e] : 0, n = live ? a.shares[2 + e] - f : 0;
         const int64_t x0 = int64_t(a.c.heads) * f + int64_t(head / a.group) * n;
         const int64_t w0 = x0 / share, w1 = (x0 + n - 1) / share;
@@ -554,7 +566,8 @@ hipError_t launch_attend(const AttendArgs& a) {
     const AttendPlan& p = a.plan;
     char* ws = static_cast<char*>(a.workspace);
     AttendDev d{a.c, a.b, a.q, a.out, a.lse, reinterpret_cast<float*>(ws + p.o_off),
-                reinterpret_cast<float*>(ws + p.ml_off), reinterpret_cast<int*>(ws), p.items, a.q_heads,
+                reinterpret_cast<float*>(ws + p.ml_off), reinterpret_cast<int*>(ws), p.items,
+                p.packed ? __builtin_ctz(unsigned(p.rows)) : 0, a.q_heads,
                 a.q_heads / a.c.heads, a.c.headdim, __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows,
                 a.scale * kLog2e, a.causal, a.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks, 0, 0};
     if (p.tile) {

@@ -53,8 +53,14 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     // Where that would leave XCDs idle (0), every XCD takes row tiles of all columns.
     const int wg = int(block_id());
     if (wg >= a.grid) return;
+    const int H = a.c.heads;
     int64_t id, rt;
-    if (a.columns) {
+    if (a.packed) {  // (later row tiles, with a causal mask the longer, first)
+        const int each = H * a.splits;
+        const Unit u = pair_of(a, (int(a.blocks) - 1 - wg) / each);
+        rt = u.at;
+        id = u.i * each + wg % each;
+    } else if (a.columns) {
         const int x = wg & 7, l = wg >> 3;
         const int mine = int((a.blocks / a.row_tiles - x + 7) / 8);  // columns of this XCD
         const int at = l / int(a.columns * a.row_tiles), in = l % int(a.columns * a.row_tiles);
@@ -69,11 +75,11 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     }
     const int split = int(id % a.splits);
     id /= a.splits;
-    const int H = a.c.heads, h = int(id % H);
+    const int h = int(id % H);
     const int64_t i = id / H;
     const Seq sq = seq_of(a.b, i);
     const int rows = sq.n * a.group;
-    if (rt * a.rows >= rows) return;
+    if (rt < 0 || rt * a.rows >= rows) return;
     const int r0 = int(rt) * a.rows;
     const int64_t base = sq.base;
     const Span sp = span_of(a, sq, r0);
@@ -438,7 +444,7 @@ hipError_t launch_attend_tile(const AttendDev& of, m3_dtype io, hipStream_t s) {
     const int64_t columns = d.blocks / d.row_tiles, each = (columns + 7) / 8;
     d.columns = 0;
     d.grid = d.blocks;
-    if ((columns % 8 == 0 || columns >= 64) && 8 * each * d.row_tiles <= INT32_MAX) {
+    if (!d.packed && (columns % 8 == 0 || columns >= 64) && 8 * each * d.row_tiles <= INT32_MAX) {
         const int64_t fit = (int64_t(4) << 20) / (d.split_tiles * kTile * 2 * d.D);
         d.columns = int(std::min(each, std::max<int64_t>(1, fit)));
         d.grid = 8 * each * d.row_tiles;

@@ -17,8 +17,8 @@ def ints(*v):
 
 
 def test_a_long_prompt_in_a_large_batch():
-    """2047 single tokens, then a prompt of 131072: 2^24 + 2^11 workgroups of append, 2^24 of attend. The prompt and
-    single tokens are checked at both ends; keys 64 back are seen."""
+    """2047 single tokens, then a prompt of 131072: with the longest for every sequence 2^24 + 2^11 workgroups of append,
+    2^24 of attend. The prompt and single tokens are checked at both ends; keys 64 back are seen."""
     b, L, H, D, page, window = 2048, 131072, 8, 16, 1024, 64
     g = gen(1)
     T = b - 1 + L
