@@ -1,72 +1,25 @@
 // m3_attn_host.cpp -- the C entry points of the attention layer (m3_attn.h):
 // argument checks, planning and dispatch. Host code only; every check runs
 // before the first HIP call.
-#include <algorithm>
 #include <cmath>
-#include <cstdlib>
-#include <cstring>
 
 #include "m3_attn_internal.h"
+#include "m3_host_checks.h"
 
 namespace {
 
+using m3::aligned;
+using m3::check_dtype;
+using m3::covered;
+using m3::dense;
+using m3::io_size;
+using m3::overlaps;
+using m3::Range;
+using m3::rows_overlap;
 using m3::set_error;
 
 // the thread's error detail is cleared at entry, as by every call of the library
 void clear_error() { set_error(M3_OK, "%s", ""); }
-
-size_t io_size(m3_dtype t) { return t == M3_BF16 ? 2 : 4; }
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-m3_status check_dtype(m3_dtype t) {
-    if (t != M3_F32 && t != M3_BF16) return set_error(M3_EDTYPE, "unknown io dtype %d", (int)t);
-    return M3_OK;
-}
-
-struct Range {
-    const char* name;
-    uintptr_t lo, hi;
-};
-bool overlaps(const Range& a, const Range& b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-Range dense(const char* name, const void* p, size_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{name, lo, p ? lo + bytes : lo};
-}
-// the bytes that rows cover, first to last
-Range covered(const char* name, const m3_rows& r, int64_t tokens, int64_t heads, int64_t D, size_t es) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(r.p);
-    if (!r.p || tokens == 0) return Range{name, lo, lo};
-    return Range{name, lo, lo + size_t((tokens - 1) * r.token_stride + (heads - 1) * r.head_stride + D) * es};
-}
-
-// Whether two sets of rows share bytes. Parts of one fused projection interleave: by token
-// (each part's heads together within a token stride; the common case, told by the parts'
-// places in it) or by head as well ([token][head][part][D]). Rows of the same strides share
-// bytes where some difference of their tokens and heads brings two of them closer than D.
-bool rows_overlap(const m3_rows& a, int64_t a_heads, const m3_rows& b, int64_t b_heads, int64_t tokens, int64_t D,
-                  size_t es) {
-    if (!overlaps(covered("", a, tokens, a_heads, D, es), covered("", b, tokens, b_heads, D, es))) return false;
-    const int64_t at = int64_t(reinterpret_cast<uintptr_t>(b.p)) - int64_t(reinterpret_cast<uintptr_t>(a.p));  // bytes
-    if (tokens > 1 && a.token_stride != b.token_stride) return true;  // (not told apart: taken to overlap)
-    const int64_t ts = a.token_stride * int64_t(es), row = D * int64_t(es);
-    const int64_t ea = (a_heads - 1) * a.head_stride * int64_t(es) + row, eb = (b_heads - 1) * b.head_stride * int64_t(es) + row;
-    if (tokens > 1 && ea <= ts && eb <= ts) {
-        int64_t off = at % ts;
-        if (off < 0) off += ts;
-        if (off >= ea && off + eb <= ts) return false;
-    }
-    if (a_heads > 1 && b_heads > 1 && a.head_stride != b.head_stride) return true;
-    const int64_t hs = (a_heads > 1 ? a : b).head_stride * int64_t(es);
-    for (int64_t h = 1 - b_heads; h < a_heads; ++h) {  // a's head less b's
-        const int64_t gap = at - h * hs;                // what the tokens' difference would have to make up
-        int64_t t = tokens > 1 && ts > 0 ? gap / ts : 0;
-        for (int64_t d = t - 1; d <= t + 1; ++d) {
-            const int64_t n = std::max(1 - tokens, std::min(tokens - 1, d));
-            if (std::abs(gap - n * ts) < row) return true;
-        }
-    }
-    return false;
-}
 
 constexpr int64_t kMaxStride = int64_t(1) << 31;  // times 2^30 tokens and 4 bytes: still within 64 bits
 

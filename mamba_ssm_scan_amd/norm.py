@@ -1,0 +1,220 @@
+"""The joint between two blocks of a hybrid stack: residual, gate, scale and the norms on either side, with gradients.
+
+torch tensors in, the C entry points of include/m3_norm.h called, as in `binding`: argument marshalling only, outputs
+and workspaces allocated with torch on the call's stream, no other implementation behind it.
+
+    y = norm.residual_norm(x, weight=w)                          # the first block's input: the stream's norm
+    o = block(y)
+    x, y = norm.residual_norm(x, o, weight=w2)                   # x + o, and the next block's input
+    x, y = norm.residual_norm(x, o, gate=g, scale=s, post_weight=w1, weight=w2)   # o normed, gated, scaled
+    x = norm.residual_norm(x, o)                                 # after the last block
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import binding
+from .attention import _dense, _device_of, _handle, _on_stream
+from .binding import check
+
+GATES = {"identity": 0, "silu": 1, "sigmoid": 2}
+
+# every symbol include/m3_norm.h declares
+EXPORTS = ["m3_residual_norm", "m3_residual_norm_backward", "m3_residual_norm_backward_workspace_size"]
+
+_vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+
+
+class M3Lines(ctypes.Structure):
+    _fields_ = [("p", _vp), ("stride", _i64)]
+
+
+class M3Joint(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("width", _i32), ("stream_dtype", _i32), ("io_dtype", _i32),
+                ("gate_fn", _i32), ("eps", _f32), ("factor", _f32), ("scale", _vp), ("post_weight", _vp), ("weight", _vp)]
+
+
+_ready = None
+
+
+def _lib():
+    global _ready
+    if _ready is None:
+        lib = binding.load()
+        joint, lines = ctypes.POINTER(M3Joint), ctypes.POINTER(M3Lines)
+        lib.m3_residual_norm.argtypes = [joint] + [lines] * 5 + [_vp]
+        lib.m3_residual_norm.restype = ctypes.c_int
+        lib.m3_residual_norm_backward.argtypes = [joint] + [lines] * 8 + [_vp] * 4 + [_sz, _vp]
+        lib.m3_residual_norm_backward.restype = ctypes.c_int
+        lib.m3_residual_norm_backward_workspace_size.argtypes = [joint, _i32]
+        lib.m3_residual_norm_backward_workspace_size.restype = _sz
+        _ready = lib
+    return _ready
+
+
+def _lines(t, name: str, device, dtype, shape) -> Optional[M3Lines]:
+    """Rows [..., width] where they lie: the entries of a row contiguous, the rows at one stride."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dim() == 2 or not t.numel():
+        st = t.stride()
+        if t.numel() and st[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"{name}: the entries of a row must be contiguous")
+        return M3Lines(t.data_ptr(), st[0] if t.dim() == 2 else shape[-1])
+    try:
+        rows = t.detach().view(-1, shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}: its rows must lie at one stride") from None
+    return _lines(rows, name, device, dtype, rows.shape)
+
+
+def _joint(x_dtype, o_dtype, shape, device, gate_fn, scale, post_weight, weight, eps) -> M3Joint:
+    if not shape:
+        raise ValueError("rows must be [..., width]")
+    W = shape[-1]
+    T = 1
+    for n in shape[:-1]:
+        T *= n
+    if gate_fn not in GATES:
+        raise ValueError(f"unknown gate_fn {gate_fn!r}: {', '.join(GATES)}")
+    factor, vec = 1.0, None
+    if isinstance(scale, torch.Tensor):
+        vec = _dense(scale, "scale", device, torch.float32, (W,))
+    elif scale is not None:
+        factor = float(scale)
+    pw = None if post_weight is None else _dense(post_weight, "post_weight", device, torch.float32, (W,))
+    w = None if weight is None else _dense(weight, "weight", device, torch.float32, (W,))
+    return M3Joint(T, W, binding._io_code(x_dtype), binding._io_code(o_dtype), GATES[gate_fn], eps, factor, vec, pw, w)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    """residual_norm as a step of autograd; the gradients are not differentiable again."""
+
+    @staticmethod
+    def forward(ctx, x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype):
+        ctx.set_materialize_grads(False)
+        vec = scale if isinstance(scale, torch.Tensor) else None
+        got = _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, None, dtype)
+        h = x if o is None else got[0] if weight is not None else got
+        ctx.save_for_backward(h if weight is not None else None, o, gate, vec, post_weight, weight)
+        ctx.how = (gate_fn, eps, scale if vec is None else None)
+        return got
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        h, o, gate, scale, post_weight, weight = ctx.saved_tensors
+        gate_fn, eps, factor = ctx.how
+        dh = grads[0] if o is not None else None
+        dy = grads[-1] if weight is not None else None
+        if dh is None and dy is None:
+            return (None,) * 9
+        rows = lambda t: None if t is None else t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()  # noqa: E731
+        need = ctx.needs_input_grad
+        g = residual_norm_backward(rows(dh), rows(dy), h if dy is not None else None, o, gate=gate, gate_fn=gate_fn,
+                                   scale=factor if scale is None else scale, post_weight=post_weight,
+                                   weight=weight if dy is not None else None, eps=eps,
+                                   want=[k for k, n in zip(_GRADS, need) if n and not (k == "weight" and dy is None)])
+        return tuple(g[k] for k in _GRADS) + (None, None, None)
+
+
+_GRADS = ("x", "o", "gate", "scale", "post_weight", "weight")
+
+
+@_on_stream
+def _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype):
+    dev = _device_of(x, "x")
+    if o is None and (gate is not None or out is not None):
+        raise ValueError("gate or out without o")
+    if out is None and torch.is_grad_enabled() and any(
+            isinstance(t, torch.Tensor) and t.requires_grad for t in (x, o, gate, scale, post_weight, weight)):
+        return _ResidualNorm.apply(x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype)
+    shape, xt = x.shape, x.dtype
+    ot = getattr(o, "dtype", None) if o is not None else xt if dtype is None else dtype
+    if dtype is not None and dtype is not ot:
+        raise ValueError(f"dtype {dtype} beside an o of {ot}")
+    j = _joint(xt, ot, shape, dev, gate_fn, scale, post_weight, weight, eps)
+    rx = _lines(x, "x", dev, xt, shape)
+    ro = rg = rh = ry = None
+    h = y = None
+    if o is not None:
+        ro, rg = _lines(o, "o", dev, ot, shape), _lines(gate, "gate", dev, ot, shape)
+        h = x.new_empty(shape) if out is None else out
+        rh = _lines(h, "out", dev, xt, shape)
+    if weight is not None:
+        y = x.new_empty(shape, dtype=ot)
+        ry = _lines(y, "y", dev, ot, shape)
+    check(_lib().m3_residual_norm(j, rx, ro, rg, rh, ry, _handle(dev)))
+    return y if o is None else h if weight is None else (h, y)
+
+
+def residual_norm(x, o=None, *, gate=None, gate_fn: str = "silu", scale=None, post_weight=None, weight=None,
+                  eps: float = 1e-6, out=None, dtype=None, stream=None):
+    """m3_residual_norm: h = x + scale * a(gate) * N(o; post_weight) and y = N(h; weight); returns (h, y), h alone
+    without weight, or y = N(x; weight) alone without o.
+
+    x [..., width] the residual stream (fp32 or bf16), o and gate of its shape (bf16, or fp32 beside an fp32 stream);
+    parts of a fused projection are used where they lie. gate_fn: "silu", "sigmoid" or "identity". scale: fp32
+    [width] or a number. post_weight, weight: fp32 [width]; without post_weight o is not normed. Norms are of the
+    root mean square, N(v; w) = v w / sqrt(mean v^2 + eps). width: up to 8192. out: where h goes, may be x itself.
+    dtype: y's type without o (x's unless given; with o it is o's). stream: the current one unless given. The results take part in autograd where an input does, unless out is given
+    (as in torch, a backward pass is captured into a graph only while no eager graph of the same leaves lives).
+    """
+    return _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype, stream=stream)
+
+
+@_on_stream
+def _backward(first, dh, dy, h, o, gate, gate_fn, scale, post_weight, weight, eps, want):
+    dev, shape = first.device, first.shape
+    xt = h.dtype if h is not None else dh.dtype
+    ot = o.dtype if o is not None else dy.dtype
+    j = _joint(xt, ot, shape, dev, gate_fn, scale, post_weight, weight, eps)
+    given = {"x": True, "o": o is not None, "gate": gate is not None, "scale": o is not None and j.scale,
+             "post_weight": o is not None and j.post_weight, "weight": j.weight}
+    ins = [_lines(t, n, dev, d, shape) for t, n, d in ((dh, "dh", xt), (dy, "dy", ot), (h, "h", xt), (o, "o", ot),
+                                                       (gate, "gate", ot))]
+    g = dict.fromkeys(_GRADS)
+    for k in _GRADS if want is None else want:
+        if k not in given:
+            raise ValueError(f"no gradient {k!r}: {', '.join(_GRADS)}")
+        if given[k]:
+            g[k] = (first.new_empty(shape, dtype=xt if k == "x" else ot) if k in ("x", "o", "gate") else
+                    first.new_empty(shape[-1], dtype=torch.float32))
+    if all(t is None for t in g.values()):
+        return g
+    outs = [_lines(g[k], "d" + k, dev, xt if k == "x" else ot, shape) for k in ("x", "o", "gate")]
+    sums = [None if g[k] is None else g[k].data_ptr() for k in ("weight", "post_weight", "scale")]
+    lib = _lib()
+    n = lib.m3_residual_norm_backward_workspace_size(j, any(p is not None for p in sums))
+    ws = first.new_empty(n, dtype=torch.uint8) if n else None
+    check(lib.m3_residual_norm_backward(j, *ins, *outs, *sums, ws.data_ptr() if n else None, n, _handle(dev)))
+    return g
+
+
+def residual_norm_backward(dh, dy, h, o=None, *, gate=None, gate_fn: str = "silu", scale=None, post_weight=None,
+                           weight=None, eps: float = 1e-6, want=None, stream=None):
+    """m3_residual_norm_backward: the gradients at stream h (the h that residual_norm returned; x without o), as a
+    dict with the keys x, o, gate (rows), scale, post_weight, weight (fp32 [width]); None where there is no such input.
+
+    dh, dy: the gradients of h and y, of their types; either may be None (dy without weight). Without dy, h is not
+    needed. want: the keys to form, all unless given. stream: the current one unless given.
+    """
+    if (dy is None) != (weight is None):
+        raise ValueError("dy and weight must be given together")
+    if dh is None and dy is None:
+        raise ValueError("neither dh nor dy is given")
+    if dy is not None and h is None:
+        raise ValueError("dy without h")
+    first = dh if dh is not None else dy
+    _device_of(first, "dh" if dh is not None else "dy")
+    return _backward(first, dh, dy, h if dy is not None else None, o, gate, gate_fn, scale, post_weight, weight, eps, want,
+                     stream=stream)
