@@ -177,6 +177,43 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
 size_t m3_kv_attend_workspace_size(const m3_kv_cache* cache, const m3_kv_batch* batch, int32_t q_heads,
                                    m3_dtype io_dtype, int32_t causal, int64_t window);
 
+/*
+ * What rows see, beyond causal and window of m3_kv_attend: first tokens that stay visible
+ * under a window, and first pages that sequences hold together.
+ * sinks: with a window, a row at position p sees the keys j <= p with j > p - window or j <
+ * sinks (without one it sees them all the same). Pages that hold none of either are not read: their
+ * entries may name anything.
+ * groups > 0: sequences group_start[g] .. group_start[g + 1] - 1 hold their first prefix_count[g] pages (whole
+ * pages, all full) together; prefix_pages[g] names them, and the sequences' own entries for them
+ * are not read. Positions and lengths count the prefix, and batch->max_pages covers it. A
+ * sequence of no group shares nothing. group_start NULL: one group (groups 1) of all sequences.
+ * Device arrays are int32; group_start does not decrease. A count outside 0 .. max_prefix is
+ * taken to the nearer end.
+ */
+typedef struct m3_kv_view {
+    int32_t causal;
+    int64_t window;              /* 0: none */
+    int64_t sinks;               /* >= 0 */
+    int64_t groups;              /* 0: no prefixes */
+    int64_t max_prefix;          /* pages of a row of prefix_pages */
+    const int32_t* group_start;  /* [groups + 1] or NULL */
+    const int32_t* prefix_count; /* [groups] */
+    const int32_t* prefix_pages; /* [groups][max_prefix] */
+} m3_kv_view;
+
+/*
+ * m3_kv_attend_view -- m3_kv_attend over such a view. The outputs are those of m3_kv_attend over tables that name
+ * the shared pages themselves (up to the order of fp32 sums); the prefix of a group is read once
+ * for many of its rows where that pays.
+ */
+m3_status m3_kv_attend_view(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_kv_view* view,
+                            const m3_rows* q, void* out, float* lse, int32_t q_heads, m3_dtype io_dtype, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes m3_kv_attend_view needs (0 on invalid sizes). Host only; device arrays are not read. */
+size_t m3_kv_attend_view_workspace_size(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_kv_view* view,
+                                        int32_t q_heads, m3_dtype io_dtype);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,8 @@ BLOCK = 16  # tokens that share a scale, per head
 FORMATS = {torch.int8: M3_KV_INT8, torch.float8_e4m3fn: M3_KV_FP8}
 
 # every symbol include/m3_attn.h declares
-EXPORTS = ["m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend", "m3_kv_attend_workspace_size"]
+EXPORTS = ["m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend", "m3_kv_attend_workspace_size", "m3_kv_attend_view",
+           "m3_kv_attend_view_workspace_size"]
 
 _vp, _i32, _i64, _f32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 
@@ -52,6 +53,11 @@ class M3Rotary(ctypes.Structure):
     _fields_ = [("inv_freq", _vp), ("rot", _i32), ("interleaved", _i32), ("mscale", _f32)]
 
 
+class M3KvView(ctypes.Structure):
+    _fields_ = [("causal", _i32), ("window", _i64), ("sinks", _i64), ("groups", _i64), ("max_prefix", _i64),
+                ("group_start", _vp), ("prefix_count", _vp), ("prefix_pages", _vp)]
+
+
 _ready = None
 
 
@@ -66,7 +72,11 @@ def _lib():
         lib.m3_kv_attend.argtypes = [cache, batch, rows, _vp, _vp, _i32, ctypes.c_int, _f32, _i32, _i64, _vp, _sz, _vp]
         lib.m3_kv_attend_workspace_size.argtypes = [cache, batch, _i32, ctypes.c_int, _i32, _i64]
         lib.m3_kv_attend_workspace_size.restype = _sz
-        for name in ("m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend"):
+        view = ctypes.POINTER(M3KvView)
+        lib.m3_kv_attend_view.argtypes = [cache, batch, view, rows, _vp, _vp, _i32, ctypes.c_int, _f32, _vp, _sz, _vp]
+        lib.m3_kv_attend_view_workspace_size.argtypes = [cache, batch, view, _i32, ctypes.c_int]
+        lib.m3_kv_attend_view_workspace_size.restype = _sz
+        for name in ("m3_rope", "m3_kv_append", "m3_kv_read", "m3_kv_attend", "m3_kv_attend_view"):
             getattr(lib, name).restype = ctypes.c_int
         _ready = lib
     return _ready
@@ -214,6 +224,31 @@ def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1
     return out
 
 
+class SharedPrefix:
+    """First pages that the sequences of a group hold together, for `KVCache.attend`.
+
+    pages [groups][max_prefix] int32 names each group's pages, count [groups] int32 how many of them (whole, full pages)
+    its sequences share; cu_seqs [groups + 1] int32 the groups' sequences, cu_seqs[g] .. cu_seqs[g + 1] - 1 (None: one
+    group of the whole batch). The sequences' positions, lengths and own page tables count the prefix as ever; their
+    own entries for its pages are not read. A sequence outside every group shares nothing. The tensors may change
+    between calls, their sizes not.
+    """
+
+    def __init__(self, pages, count, cu_seqs=None):
+        dev = _device_of(pages, "pages")
+        _dense(pages, "pages", dev, torch.int32)
+        if pages.dim() != 2:
+            raise ValueError("pages must be [groups][max_prefix]")
+        g = pages.shape[0]
+        _dense(count, "count", dev, torch.int32, (g,))
+        if cu_seqs is not None:
+            _dense(cu_seqs, "cu_seqs", dev, torch.int32, (g + 1,))
+        elif g != 1:
+            raise ValueError(f"{g} groups need cu_seqs")
+        self.pages, self.count, self.cu_seqs, self.device = pages, count, cu_seqs, dev
+        self._c = (g, pages.shape[1], cu_seqs.data_ptr() if cu_seqs is not None else None, count.data_ptr(), pages.data_ptr())
+
+
 class KVCache:
     """A paged cache of keys and values in 8 bits, one scale per 16 tokens and head (the layout of m3_kv_cache).
 
@@ -324,11 +359,14 @@ class KVCache:
 
     @_on_stream
     def attend(self, q, kv_len, pages, *, cu_q=None, max_q: Optional[int] = None, max_kv: Optional[int] = None,
-               scale: Optional[float] = None, causal: bool = True, window: int = 0, out=None, lse=False):
-        """m3_kv_attend: q [tokens][q_heads][dim] over the cache; returns out, or (out, lse) with lse=True.
+               scale: Optional[float] = None, causal: bool = True, window: int = 0, sinks: int = 0,
+               prefix: Optional[SharedPrefix] = None, out=None, lse=False):
+        """m3_kv_attend_view: q [tokens][q_heads][dim] over the cache; returns out, or (out, lse) with lse=True.
 
         scale: 1 / sqrt(dim) unless given. causal: a row sees the keys up to its own position; window > 0: only the
-        last `window` of them. A row that sees nothing gives 0 (and lse -inf). max_kv: at least the largest kv_len,
+        last `window` of them, and the first `sinks` of its sequence (pages with neither are not read, their entries
+        in `pages` may be anything). prefix: first pages that sequences hold together, read once for many of them where
+        that pays. A row that sees nothing gives 0 (and lse -inf). max_kv: at least the largest kv_len,
         the page table's room unless given. stream: the current one unless given.
         """
         dev, dt = self.device, q.dtype
@@ -346,14 +384,19 @@ class KVCache:
             out = q.new_empty(shape)
         o = _dense(out, "out", dev, dt, shape)
         z = q.new_empty((T, H), dtype=torch.float32) if lse else None
-        causal = 1 if causal else 0
-        key = (b.batch, T, b.max_pages, b.max_q, b.max_kv, cu_q is None, H, code, causal, window)
+        shared = (0, 0, None, None, None)
+        if prefix is not None:
+            if prefix.device != dev:
+                raise ValueError(f"prefix must be on {dev}")
+            shared = prefix._c
+        view = M3KvView(1 if causal else 0, window, sinks, *shared)
+        key = (b.batch, T, b.max_pages, b.max_q, b.max_kv, cu_q is None, H, code, view.causal, window, sinks, *shared[:2])
         n = self._sizes.get(key)
         if n is None:
             if len(self._sizes) > 4096:
                 self._sizes.clear()
-            n = self._sizes[key] = lib.m3_kv_attend_workspace_size(self._c, b, H, code, causal, window)
+            n = self._sizes[key] = lib.m3_kv_attend_view_workspace_size(self._c, b, view, H, code)
         ws = q.new_empty(n, dtype=torch.uint8) if n else None
-        check(lib.m3_kv_attend(self._c, b, rq, o, z.data_ptr() if lse else None, H, code, scale, causal, window,
-                               ws.data_ptr() if n else None, n, _handle(dev)))
+        check(lib.m3_kv_attend_view(self._c, b, view, rq, o, z.data_ptr() if lse else None, H, code, scale,
+                                    ws.data_ptr() if n else None, n, _handle(dev)))
         return (out, z) if lse else out

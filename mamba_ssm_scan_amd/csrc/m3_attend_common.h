@@ -28,6 +28,7 @@ struct AttendDev {
     int splits;
     bool wide;
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
+    m3_kv_view view;
     // of the tile kernel's launch:
     int columns;     // (sequence, head, split)s side by side in an XCD (0: runs of workgroups)
     int64_t grid;
@@ -61,18 +62,64 @@ __device__ __forceinline__ int64_t pair_at(const AttendDev& a, int64_t i, int64_
     return a.packed ? first_unit(a.b, i, a.group, a.packed, 1) + rt : i * a.row_tiles + rt;
 }
 
-// Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see.
+// Kernels come in two forms: VIEW, for calls with sinks or prefixes, and without.
+
+// The pages that sequence i holds with others: its first `count`, named by `pages`.
+struct Prefix {
+    const int32_t* pages;
+    int count;
+};
+__device__ __forceinline__ Prefix prefix_of(const AttendDev& a, int64_t i) {
+    const m3_kv_view& v = a.view;
+    if (v.groups == 0) return Prefix{nullptr, 0};
+    int64_t g = 0;
+    if (v.group_start) {  // the last group that begins at or before i
+        for (int64_t hi = v.groups - 1; g < hi;) {
+            const int64_t mid = (g + hi + 1) / 2;
+            if (v.group_start[mid] <= i) g = mid;
+            else hi = mid - 1;
+        }
+        if (i < v.group_start[g] || i >= v.group_start[g + 1]) return Prefix{nullptr, 0};
+    }
+    return Prefix{v.prefix_pages + g * v.max_prefix, min(max(v.prefix_count[g], 0), int(v.max_prefix))};
+}
+
+// Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see: number t of lo .. hi
+// - 1 is tile t, under sinks tile t + skip from the first that the window shows on.
 struct Span {
     int64_t lo, hi;
+    int sinks, skip;  // (VIEW) tiles of the sinks alone, tiles between them and the window's
 };
+// Keeps what is computed from a register after this point, where the compiler would form it
+// early and hold it.
+__device__ __forceinline__ unsigned here(unsigned w) {
+    asm volatile("" : "+v"(w));
+    return w;
+}
+template <bool VIEW>
+__device__ __forceinline__ int tile_at(const Span& sp, int t) {
+    if constexpr (VIEW) return t < sp.sinks ? t : t + sp.skip;
+    else return t;
+}
+template <bool VIEW>
 __device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0) {
     const int r1 = min(r0 + a.rows, s.n * a.group) - 1;
     const int64_t base = s.base;
     int64_t hi = min(int64_t(s.held), a.b.max_kv), lo = 0;
     if (a.causal) hi = min(hi, base + r1 / a.group + 1);
     if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);
-    if (hi <= lo) return Span{0, 0};
-    return Span{lo / kTile, (hi + kTile - 1) / kTile};
+    if constexpr (VIEW) {
+        const int64_t first = min(min(a.view.sinks, lo), hi);  // keys that only sinks show
+        if (hi <= lo && first <= 0) return Span{0, 0, 0, 0};
+        const int sinks = int((max(first, int64_t(0)) + kTile - 1) / kTile);
+        if (hi <= lo) return Span{0, sinks, sinks, 0};
+        const int from = int(lo / kTile), to = int((hi + kTile - 1) / kTile);
+        const int skip = max(from - sinks, 0);
+        return Span{0, to - skip, sinks, skip};
+    } else {
+        if (hi <= lo) return Span{0, 0, 0, 0};
+        return Span{lo / kTile, (hi + kTile - 1) / kTile, 0, 0};
+    }
 }
 
 // How the kernel for many rows cuts a row tile's keys: into as many pieces as the plan has

@@ -111,18 +111,39 @@ m3_kv_batch bounded(const m3_kv_batch& b, const m3_kv_cache& c) {
     return r;
 }
 
-// a window that no position reaches the end of, so that sums with it stay in range
-int64_t bounded(int64_t window) { return std::min(window, int64_t(1) << 31); }
+// the plain view of m3_kv_attend
+m3_kv_view plain(int32_t causal, int64_t window) { return m3_kv_view{causal ? 1 : 0, window, 0, 0, 0, nullptr, nullptr, nullptr}; }
+// A view whose window's end no position reaches, so that sums with it stay in range; as for
+// sinks; and prefixes that end within 32 bits.
+m3_kv_view bounded(const m3_kv_view& v, const m3_kv_cache& c) {
+    m3_kv_view r = v;
+    r.causal = v.causal ? 1 : 0;
+    r.window = std::min(v.window, int64_t(1) << 31);
+    r.sinks = v.window > 0 ? std::min(v.sinks, (int64_t(1) << 31) - 256) : 0;  // (as max_kv)
+    r.max_prefix = std::min(v.max_prefix, ((int64_t(1) << 31) - 256) / c.page_size);
+    if (r.max_prefix == 0) r.groups = 0;
+    return r;
+}
 
-m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, int32_t q_heads, m3_dtype io, int32_t causal,
-                       int64_t window) {
+m3_status check_attend(const m3_kv_cache* c, const m3_kv_batch* b, const m3_kv_view* v, int32_t q_heads, m3_dtype io) {
     m3_status s;
     if ((s = check_cache(c)) != M3_OK || (s = check_batch(b)) != M3_OK || (s = check_dtype(io)) != M3_OK) return s;
+    if (!v) return set_error(M3_EINVAL, "view is NULL");
     if (q_heads < 1 || q_heads > 65536 || q_heads % c->heads != 0)
         return set_error(M3_EINVAL, "q_heads %d must be a multiple of the cache's heads %d", q_heads, c->heads);
-    if (window < 0) return set_error(M3_EINVAL, "window %lld < 0", (long long)window);
-    if (window > 0 && !causal) return set_error(M3_EUNSUPPORTED, "a window needs causal attention");
+    if (v->window < 0) return set_error(M3_EINVAL, "window %lld < 0", (long long)v->window);
+    if (v->window > 0 && !v->causal) return set_error(M3_EUNSUPPORTED, "a window needs causal attention");
     if (b->tokens * q_heads > INT32_MAX) return set_error(M3_EUNSUPPORTED, "tokens * q_heads is above 2^31");
+    if (v->sinks < 0) return set_error(M3_EINVAL, "sinks %lld < 0", (long long)v->sinks);
+    if (v->groups < 0 || v->groups > (int64_t(1) << 30) || v->max_prefix < 0 || v->max_prefix > (int64_t(1) << 31))
+        return set_error(M3_EINVAL, "groups %lld or max_prefix %lld out of range", (long long)v->groups,
+                         (long long)v->max_prefix);
+    if (v->groups == 0) return M3_OK;
+    if (!v->group_start && v->groups != 1) return set_error(M3_EINVAL, "group_start is NULL, but there are %lld groups", (long long)v->groups);
+    if (!v->prefix_count) return set_error(M3_EINVAL, "prefix_count is NULL");
+    if (!v->prefix_pages && v->max_prefix > 0) return set_error(M3_EINVAL, "prefix_pages is NULL");
+    if (!aligned(v->group_start, 4) || !aligned(v->prefix_count, 4) || !aligned(v->prefix_pages, 4))
+        return set_error(M3_EALIGN, "group_start, prefix_count or prefix_pages is not 4-byte aligned");
     return M3_OK;
 }
 
@@ -162,9 +183,11 @@ namespace m3 {
 // sequences first, a column's in one XCD). Under a bound of all rows instead of the
 // longest's: 128 single tokens over 2100 57 us and 49 (187 by the bound alone), 64 prompts
 // of 300 113 and 100 (402), 4 prompts of 2048 108 and 107 (142 with the pairs packed).
-AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
-                       int64_t window) {
+AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
+                       m3_dtype io) {
     AttendPlan p{};
+    const int32_t causal = view.causal;
+    const int64_t window = view.window;
     const int64_t group = q_heads / c.heads;
     // what a sequence's rows are taken to be: the bound, or four times the mean below it
     const int64_t mean = b.cu_q && b.batch > 0 ? (b.tokens + b.batch - 1) / b.batch : 1;
@@ -180,7 +203,7 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_hea
     p.row_tiles = each(p.rows);
     p.packed = b.cu_q && (p.tile ? 8 : 2) * packed(p.rows) <= b.batch * p.row_tiles;
     int64_t tiles = (b.max_kv + 63) / 64;
-    if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1);
+    if (window > 0) tiles = std::min(tiles, (window + (p.rows - 1) / group + 1 + 62) / 64 + 1 + (view.sinks + 63) / 64);
     tiles = std::max<int64_t>(1, tiles);
     const int64_t items = p.packed ? packed(p.rows) : b.batch * p.row_tiles, base = std::max<int64_t>(1, items * c.heads);
     const int64_t busy = std::max<int64_t>(1, std::min(items, b.cu_q ? packed(p.rows) : items) * c.heads);
@@ -338,16 +361,29 @@ m3_status m3_kv_read(const m3_kv_cache* cache, int64_t batch, const int32_t* fir
 
 size_t m3_kv_attend_workspace_size(const m3_kv_cache* cache, const m3_kv_batch* batch, int32_t q_heads,
                                    m3_dtype io_dtype, int32_t causal, int64_t window) {
+    const m3_kv_view view = plain(causal, window);
+    return m3_kv_attend_view_workspace_size(cache, batch, &view, q_heads, io_dtype);
+}
+
+size_t m3_kv_attend_view_workspace_size(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_kv_view* view,
+                                        int32_t q_heads, m3_dtype io_dtype) {
     clear_error();
-    if (check_attend(cache, batch, q_heads, io_dtype, causal, window) != M3_OK) return 0;
-    return m3::attend_plan(*cache, bounded(*batch, *cache), q_heads, io_dtype, causal, bounded(window)).total;
+    if (check_attend(cache, batch, view, q_heads, io_dtype) != M3_OK) return 0;
+    return m3::attend_plan(*cache, bounded(*batch, *cache), bounded(*view, *cache), q_heads, io_dtype).total;
 }
 
 m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_rows* q, void* out, float* lse,
                        int32_t q_heads, m3_dtype io_dtype, float scale, int32_t causal, int64_t window,
                        void* workspace, size_t workspace_bytes, void* stream) {
+    const m3_kv_view view = plain(causal, window);
+    return m3_kv_attend_view(cache, batch, &view, q, out, lse, q_heads, io_dtype, scale, workspace, workspace_bytes, stream);
+}
+
+m3_status m3_kv_attend_view(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_kv_view* view,
+                            const m3_rows* q, void* out, float* lse, int32_t q_heads, m3_dtype io_dtype, float scale,
+                            void* workspace, size_t workspace_bytes, void* stream) {
     clear_error();
-    m3_status s = check_attend(cache, batch, q_heads, io_dtype, causal, window);
+    m3_status s = check_attend(cache, batch, view, q_heads, io_dtype);
     if (s != M3_OK) return s;
     const size_t es = io_size(io_dtype);
     const int64_t T = batch->tokens, D = cache->headdim;
@@ -356,9 +392,9 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
     if (!aligned(out, 16)) return set_error(M3_EALIGN, "out is not 16-byte aligned");
     if (!aligned(lse, 4)) return set_error(M3_EALIGN, "lse is not 4-byte aligned");
     if (!std::isfinite(scale)) return set_error(M3_EINVAL, "scale is not finite");
-    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, causal ? 1 : 0,
-                     bounded(window), {}, workspace, wide_rows(*q, es), reinterpret_cast<hipStream_t>(stream)};
-    a.plan = m3::attend_plan(*cache, a.b, q_heads, io_dtype, causal, a.window);
+    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, bounded(*view, *cache),
+                     {}, workspace, wide_rows(*q, es), reinterpret_cast<hipStream_t>(stream)};
+    a.plan = m3::attend_plan(*cache, a.b, a.view, q_heads, io_dtype);
     const size_t rows = size_t(T) * size_t(q_heads);
     const Range outs[] = {dense("out", out, rows * size_t(D) * es), dense("lse", lse, rows * 4),
                           dense("workspace", workspace, workspace_bytes)};
@@ -367,7 +403,10 @@ m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const
                         dense("pages", batch->pages, size_t(batch->batch) * size_t(batch->max_pages) * 4),
                         dense("cache k", cache->k, cache_codes(*cache)), dense("cache v", cache->v, cache_codes(*cache)),
                         dense("cache k_scale", cache->k_scale, cache_scales(*cache)),
-                        dense("cache v_scale", cache->v_scale, cache_scales(*cache))};
+                        dense("cache v_scale", cache->v_scale, cache_scales(*cache)),
+                        dense("group_start", view->group_start, size_t(view->groups + 1) * 4),
+                        dense("prefix_count", view->prefix_count, size_t(view->groups) * 4),
+                        dense("prefix_pages", view->prefix_pages, size_t(view->groups) * size_t(view->max_prefix) * 4)};
     for (int o = 0; o < 3; ++o) {
         for (const Range& r : in)
             if (overlaps(outs[o], r)) return set_error(M3_EINVAL, "%s overlaps %s", outs[o].name, r.name);

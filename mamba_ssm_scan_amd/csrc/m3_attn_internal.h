@@ -89,15 +89,16 @@ struct AttendArgs {
     int32_t q_heads;
     m3_dtype io;
     float scale;
-    int32_t causal;
-    int64_t window;
+    m3_kv_view view;      // sinks 0 without a window, max_prefix bounded
     AttendPlan plan;
     void* workspace;
     bool wide;
     hipStream_t stream;
 };
-AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, int32_t q_heads, m3_dtype io, int32_t causal,
-                       int64_t window);
+// Whether a (bounded) view takes the kernels' VIEW form.
+inline bool has_view(const m3_kv_view& v) { return v.sinks > 0 || v.groups > 0; }
+AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
+                       m3_dtype io);
 hipError_t launch_kv_attend(const AttendArgs& a);
 
 }  // namespace m3

@@ -39,13 +39,6 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kMaxItems = kAttendItems;
 
-// Keeps what is computed from a register after this point, where the compiler would
-// convert a tile's codes early and hold them at twice or four times their size.
-__device__ __forceinline__ unsigned here(unsigned w) {
-    asm volatile("" : "+v"(w));
-    return w;
-}
-
 // Even shares. The tiles of all (sequence, row tile) items lie one after the other,
 // an item's once for each key head; a workgroup takes the same number of them,
 // whatever the lengths, and a row tile's keys that several share are joined
@@ -54,6 +47,7 @@ __device__ __forceinline__ unsigned here(unsigned w) {
 // the next part to slot 2 w. Every workgroup forms the items' first tiles itself
 // (one scan of the lengths), the first also stores them for the join. Returns the
 // tiles of a share: a multiple of 4, one tile a wave at least.
+template <bool VIEW>
 __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* scan) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int per = (a.items + 64 * kWaves - 1) / (64 * kWaves);
@@ -63,7 +57,7 @@ __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* 
         const Unit u = pair_of(a, e);
         const Seq sq = seq_of(a.b, u.i);
         const int64_t r0 = u.at * a.rows;
-        const Span sp = r0 >= 0 && r0 < sq.n * a.group ? span_of(a, sq, int(r0)) : Span{0, 0};
+        const Span sp = r0 >= 0 && r0 < sq.n * a.group ? span_of<VIEW>(a, sq, int(r0)) : Span{0, 0, 0, 0};
         first[e] = int(sp.hi - sp.lo);
         sum += int(sp.hi - sp.lo);
     }
@@ -119,14 +113,14 @@ __device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) 
 // EVEN: even shares (their bookkeeping takes registers that the other case keeps for
 // more waves).
 // Waves a SIMD: what the registers of each case allow without spilling in its loop.
-template <typename T, int DP, int QT, bool EVEN>
-constexpr int kSimdWaves = DP == 256 || (sizeof(T) == 4 && DP * QT > 128) ? 1
-                           : sizeof(T) == 4 || QT == 2                    ? 2
-                           : DP == 64                                     ? 4
-                           : EVEN                                         ? 2
-                                                                          : 3;
-template <typename T, bool FP8, int DP, int QT, bool FULL, bool EVEN>
-__global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void attend_rows_kernel(AttendDev a) {
+template <typename T, int DP, int QT, bool EVEN, bool VIEW>
+constexpr int kSimdWaves = DP == 256 || (sizeof(T) == 4 && DP * QT > 128) || (VIEW && EVEN && DP * QT > 128) ? 1
+                           : sizeof(T) == 4 || QT == 2                                                        ? 2
+                           : DP == 64                                                                         ? 4
+                           : EVEN || VIEW                                                                     ? 2
+                                                                                                              : 3;
+template <typename T, bool FP8, int DP, int QT, bool FULL, bool EVEN, bool VIEW>
+__global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN, VIEW>)) void attend_rows_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KC = DP / 64;        // 16-code pieces of a key row a lane holds
     constexpr int DT = DP / 16;        // 16-entry tiles of the output
@@ -144,7 +138,7 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
     if (w >= a.blocks) return;
     int64_t x = 0, xe = 1;  // what is left of this workgroup's share
     if constexpr (EVEN) {
-        const int share = even_shares(a, first_lds, scan_lds);
+        const int share = even_shares<VIEW>(a, first_lds, scan_lds);
         x = int64_t(w) * share;
         xe = min(x + share, int64_t(H) * first_lds[a.items]);
         zero_rows<T>(a, first_lds);
@@ -190,7 +184,7 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
         if (rt < 0 || rt * a.rows >= rows) break;  // (without shares only)
         const int r0 = int(rt) * a.rows;
         const int64_t base = sq.base;
-        const Span sp = span_of(a, sq, r0);
+        const Span sp = span_of<VIEW>(a, sq, r0);
         const int slot = t0 > 0 ? 2 * w : 2 * w + 1;
         if constexpr (EVEN) {
             t0 += int(sp.lo);
@@ -204,9 +198,15 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
         const int D = FULL ? DP : a.D;
         const int held = int(min(int64_t(sq.held), a.b.max_kv)), held_blocks = (held + 15) / 16;
         const int32_t* pages = a.b.pages + i * a.b.max_pages;
+        // (VIEW) keys that sinks show, the first block that the window does, and the shared pages
+        const int sinks = VIEW ? int(a.view.sinks) : 0, sink_blocks = (sinks + 15) / 16;
+        const int win_block = VIEW && a.window ? int(max(base + r0 / a.group - a.window + 1, int64_t(0)) / 16) : 0;
+        const Prefix pre = VIEW ? prefix_of(a, i) : Prefix{nullptr, 0};
         auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
-            if (blk >= held_blocks || (blk >> a.shift) >= a.b.max_pages) return -1;
-            const int64_t p = pages[blk >> a.shift];
+            const int pg = blk >> a.shift;
+            if (blk >= held_blocks || (!VIEW && pg >= a.b.max_pages)) return -1;  // (max_kv ends in the table)
+            if (VIEW && blk < win_block && blk >= sink_blocks) return -1;
+            const int64_t p = VIEW && pg < pre.count ? pre.pages[pg] : pages[pg];
             if (p < 0 || p >= a.c.num_pages) return -1;
             return ((int(p) * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
         };
@@ -229,8 +229,9 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
         int tile = t0 + wave;
         int vb = -1;
         if (tile < t1) {
-            vb = find(tile * 4 + g);
-            load_k(find(tile * 4 + (lr >> 2)));
+            const int at = tile_at<VIEW>(sp, tile);
+            vb = find(at * 4 + g);
+            load_k(find(at * 4 + (lr >> 2)));
         }
 
         // the rows' operands and the keys that each row sees
@@ -279,11 +280,12 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
             const bool there = vb >= 0;
             float ks = a.c.k_scale[max(vb, 0)] * a.scale2;
             VScale vs = v_scale(a.c.v_scale[max(vb, 0)]);
-            const int k0 = tile * kTile, next = tile + kWaves;
+            const int k0 = tile_at<VIEW>(sp, tile) * kTile, next = tile + kWaves;
             int kb2 = -1, vb2 = -1;
             if (next < t1) {
-                kb2 = find(next * 4 + (lr >> 2));
-                vb2 = find(next * 4 + g);
+                const int at = tile_at<VIEW>(sp, next);
+                kb2 = find(at * 4 + (lr >> 2));
+                vb2 = find(at * 4 + g);
             }
 
             floatx4 s[QT][4];
@@ -303,14 +305,14 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
             if (next < t1) load_k(kb2);
 
             // (a scale below 0 would turn the raw maximum round)
-            if (k0 < all_lo || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f) || vs.none)) {
+            if ((k0 < all_lo && (!VIEW || k0 + kTile > sinks)) || k0 + kTile > all_hi || __any(!there || !(ks >= 0.f) || vs.none)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int key = k0 + 16 * g + j;
                         const float x = __builtin_fmaf(s[qt][j / 4][j % 4], ks, vs.log2);
-                        s[qt][j / 4][j % 4] = there && key >= klo[qt] && key < khi[qt] ? x : -INFINITY;
+                        s[qt][j / 4][j % 4] = there && (key >= klo[qt] || (VIEW && key < sinks)) && key < khi[qt] ? x : -INFINITY;
                     }
                 ks = 1.f;
                 vs.log2 = 0.f;
@@ -457,7 +459,7 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, EVEN>)) void at
 
 // Joins rows' parts, in their order. Half a wave (a wave above headdim 128) takes a
 // row's parts, or `team` of them do where there are few rows (team: a power of two).
-template <typename T>
+template <typename T, bool VIEW>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team) {
     __shared__ __align__(16) float o_lds[256 * 4];
     const int D = a.D, width = D <= 128 ? 32 : 64, crews = 256 / width;
@@ -494,7 +496,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
         p1 = 2 * w0 * a.rows + rin;
         step = 2 * a.rows;
     } else {
-        const Span sp = live ? span_of(a, sq, r / a.rows * a.rows) : Span{0, 0};
+        const Span sp = live ? span_of<VIEW>(a, sq, r / a.rows * a.rows) : Span{0, 0, 0, 0};
         parts = cut_of(a, sp).pieces;
         live = live && parts > 1;
         p0 = p1 = at;
@@ -545,21 +547,27 @@ hipError_t launch_join(const AttendDev& d, hipStream_t s) {
     int team = 1;  // rows alone fill the chip from about 4 workgroups a CU
     while (team < crews && rows * team / crews < 1024) team *= 2;
     const int per = crews / team;
-    hipLaunchKernelGGL((attend_join_kernel<T>), grid_of((rows + per - 1) / per), dim3(256), 0, s, d, team);
+    const dim3 grid = grid_of((rows + per - 1) / per);
+    if (has_view(d.view)) hipLaunchKernelGGL((attend_join_kernel<T, true>), grid, dim3(256), 0, s, d, team);
+    else hipLaunchKernelGGL((attend_join_kernel<T, false>), grid, dim3(256), 0, s, d, team);
     return hipGetLastError();
 }
 
-template <typename T, bool FP8, int DP, int QT>
-void launch_rows(const AttendDev& d, hipStream_t s) {
+template <typename T, bool FP8, int DP, int QT, bool VIEW>
+void launch_rows_of(const AttendDev& d, hipStream_t s) {
     auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, grid_of(d.blocks), dim3(64 * kWaves), 0, s, d);
     };
     if (d.items)
-        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, true>)
-                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, true>);
+        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, true, VIEW>)
+                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, true, VIEW>);
     else
-        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, false>)
-                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, false>);
+        d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, false, VIEW>)
+                  : launch(attend_rows_kernel<T, FP8, DP, QT, false, false, VIEW>);
+}
+template <typename T, bool FP8, int DP, int QT>
+void launch_rows(const AttendDev& d, hipStream_t s) {
+    has_view(d.view) ? launch_rows_of<T, FP8, DP, QT, true>(d, s) : launch_rows_of<T, FP8, DP, QT, false>(d, s);
 }
 template <typename T, bool FP8>
 hipError_t launch_attend(const AttendArgs& a) {
@@ -569,7 +577,8 @@ hipError_t launch_attend(const AttendArgs& a) {
                 reinterpret_cast<float*>(ws + p.ml_off), reinterpret_cast<int*>(ws), p.items,
                 p.packed ? __builtin_ctz(unsigned(p.rows)) : 0, a.q_heads,
                 a.q_heads / a.c.heads, a.c.headdim, __builtin_ctz(unsigned(a.c.page_size / 16)), p.rows,
-                a.scale * kLog2e, a.causal, a.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks, 0, 0};
+                a.scale * kLog2e, a.view.causal, a.view.window, p.row_tiles, p.split_tiles, p.splits, a.wide, p.blocks, a.view,
+                0, 0};
     if (p.tile) {
         const hipError_t e = launch_attend_tile(d, a.io, a.stream);
         return e != hipSuccess || p.splits == 1 ? e : launch_join<T>(d, a.stream);

@@ -32,8 +32,8 @@
 namespace m3 {
 namespace {
 
-template <typename T, bool FP8, int DP, int QT, int NW>
-__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(AttendDev a) {
+template <typename T, bool FP8, int DP, int QT, int NW, bool VIEW>
+__global__ __launch_bounds__(64 * NW, DP == 64 && !(VIEW && QT == 2) ? 3 : 2) void attend_tile_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KM = DP / 32;          // MFMA steps of a score (32 entries each)
     constexpr int DT = DP / 16;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     if (rt < 0 || rt * a.rows >= rows) return;
     const int r0 = int(rt) * a.rows;
     const int64_t base = sq.base;
-    const Span sp = span_of(a, sq, r0);
+    const Span sp = span_of<VIEW>(a, sq, r0);
     int t0 = int(sp.lo), t1 = int(sp.hi);
     bool whole = true;
     if (a.splits > 1) {
@@ -152,18 +152,24 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
     struct Pages {
         int p[PC];   // page number of this wave's blocks of a tile (-1: none)
     };
+    // (VIEW) keys that sinks show, the first block that the window does, and the shared pages
+    const int sinks = VIEW ? int(a.view.sinks) : 0, sink_blocks = (sinks + 15) / 16;
+    const int win_block = VIEW && a.window ? int(max(base + r0 / a.group - a.window + 1, int64_t(0)) / 16) : 0;
+    const Prefix pre = VIEW ? prefix_of(a, i) : Prefix{nullptr, 0};
     auto find = [&](int tile) {
         Pages r;
 #pragma unroll
         for (int j = 0; j < PC; ++j) {
-            const int blk = tile * 4 + (64 * swave + NT * j) / DP;
+            const int blk = tile_at<VIEW>(sp, tile) * 4 + (64 * swave + NT * j) / DP, pg = blk >> a.shift;
             r.p[j] = -1;
-            if (tile < t1 && blk < held_blocks && (blk >> a.shift) < a.b.max_pages) r.p[j] = pages[blk >> a.shift];
+            if (VIEW && blk < win_block && blk >= sink_blocks) continue;
+            if (tile < t1 && blk < held_blocks && (VIEW || pg < a.b.max_pages))  // (max_kv ends in the table)
+                r.p[j] = VIEW && pg < pre.count ? pre.pages[pg] : pages[pg];
         }
         return r;
     };
     auto block = [&](int tile, const Pages& pg, int j) -> int64_t {
-        const int blk = tile * 4 + (64 * swave + NT * j) / DP;
+        const int blk = tile_at<VIEW>(sp, tile) * 4 + (64 * swave + NT * j) / DP;
         const int64_t page = __builtin_amdgcn_readfirstlane(pg.p[j]);
         if (page < 0 || page >= a.c.num_pages) return -1;
         return ((page * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
@@ -213,8 +219,9 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             u32x4 v = rv[j];
             const VScale vs = v_scale(rvs[j]);
             if (vs.none) v = u32x4{0, 0, 0, 0};
-            if (tile * kTile + kTile > held) {  // codes of slots that hold no token may be anything
-                const int nv = min(max(held - (tile * kTile + 16 * blk), 0), 16);
+            const int k0 = tile_at<VIEW>(sp, tile) * kTile;
+            if (k0 + kTile > held) {  // codes of slots that hold no token may be anything
+                const int nv = min(max(held - (k0 + 16 * blk), 0), 16);
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int n = min(max(nv - 4 * w, 0), 4);
@@ -250,7 +257,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 #pragma unroll
             for (int m = 0; m < KM; ++m) score_step(buf, t, m, x);
     };
-    auto seen = [&](int tile) { return tile * kTile < w_hi && tile * kTile + kTile > w_lo; };
+    auto seen = [&](int tile) {
+        const int k0 = tile_at<VIEW>(sp, tile) * kTile;
+        return k0 < w_hi && (k0 + kTile > w_lo || (VIEW && k0 < sinks));
+    };
 
     // kAhead. In turn n the scores of tile n are in registers, V of tile n and K of tile
     // n + 1 in LDS: the products of tile n + 1's scores run beside tile n's exponentials,
@@ -287,20 +297,20 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
             fetch_k(tile + 1, pgv);
             pgv = find(tile + 2);
         }
-        const int k0 = tile * kTile;
+        const int k0 = tile_at<VIEW>(sp, tile) * kTile;
         if (seen(tile)) {
             if constexpr (!kAhead) scores(buf, s);
             const floatx4 sc = *reinterpret_cast<const floatx4*>(sc_lds[buf][g]);
             float ks = sc[0], lv = sc[1];
             const float iv = sc[2];
-            if (k0 < all_lo || k0 + kTile > all_hi || __any(sc[3] == 0.f)) {
+            if ((k0 < all_lo && (!VIEW || k0 + kTile > sinks)) || k0 + kTile > all_hi || __any(sc[3] == 0.f)) {
 #pragma unroll
                 for (int qt = 0; qt < QT; ++qt)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const int key = k0 + 16 * g + j;
                         const float v = __builtin_fmaf(s[qt][j / 4][j % 4], ks, lv);
-                        s[qt][j / 4][j % 4] = sc[3] != 0.f && key >= klo[qt] && key < khi[qt] ? v : -INFINITY;
+                        s[qt][j / 4][j % 4] = sc[3] != 0.f && (key >= klo[qt] || (VIEW && key < sinks)) && key < khi[qt] ? v : -INFINITY;
                     }
                 ks = 1.f;
                 lv = 0.f;
@@ -418,7 +428,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void attend_tile_kernel(
 template <typename T, bool FP8, int DP, int QT, int NW>
 hipError_t launch_one(const AttendDev& d, hipStream_t s) {
     constexpr int kLds = 4 * 64 * DP * 2;
-    hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW>), grid_of(d.grid), dim3(64 * NW), kLds, s, d);
+    if (has_view(d.view)) hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW, true>), grid_of(d.grid), dim3(64 * NW), kLds, s, d);
+    else hipLaunchKernelGGL((attend_tile_kernel<T, FP8, DP, QT, NW, false>), grid_of(d.grid), dim3(64 * NW), kLds, s, d);
     return hipGetLastError();
 }
 // Rows a wave and waves (the plan's rows are their products): two tiles of 16 rows a wave where the
