@@ -26,7 +26,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
 SOURCES = ["m3_host.cpp", "m3_prefill_generic.hip", "m3_prefill_mfma.hip", "m3_decode.hip", "m3_prologue.hip",
            "m3_backward.hip", "m3_prefill_scan.hip", "m3_gate.hip", "m3_mixer.cpp", "m3_noalloc.hip",
            "m3_prefill_ws4.hip", "m3_paths.cpp", "m3_attn_host.cpp", "m3_rope.hip", "m3_kv_append.hip",
-           "m3_kv_attend.hip", "m3_kv_attend_tile.hip", "m3_norm_host.cpp", "m3_norm.hip"]
+           "m3_kv_attend.hip", "m3_kv_attend_tile.hip", "m3_kv_attend_view.hip", "m3_kv_attend_parts.hip",
+           "m3_kv_attend_tile_view.hip", "m3_norm_host.cpp", "m3_norm.hip"]
 # per-source flags: the token-walk kernel reads every MFMA result with VALU
 # ops, so its MFMAs write arch VGPRs (no accumulator-register copies)
 EXTRA = {"m3_prefill_scan.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
@@ -49,7 +50,7 @@ def _compile(src: str, verbose: bool) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(6, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs, "-L/opt/rocm/lib", "-lhipblaslt",

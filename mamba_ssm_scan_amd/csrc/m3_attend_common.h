@@ -6,6 +6,12 @@
 
 namespace m3 {
 
+// The kernels' forms: kPlain, without sinks and prefixes; kView, with them in one pass over
+// each sequence's keys; kParts, one part over a group's prefix for all its rows (a sequence
+// of keys like any other, whose rows are those of several sequences), one over each
+// sequence's own keys, brought together afterwards.
+enum Form { kPlain, kView, kParts };
+
 // A call as the kernels take it.
 struct AttendDev {
     m3_kv_cache c;
@@ -28,13 +34,25 @@ struct AttendDev {
     int splits;
     bool wide;
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
+    Form form;
     m3_kv_view view;
+    // The kParts form: the groups' (group, row tile) pairs come before the sequences' among the
+    // items, numbered by their own row tiles; where parts lie (in rows of part_o, part_ml).
+    int items_a, packed_a;
+    int64_t row_tiles_a, slots, solo_a, solo_b;
     // of the tile kernel's launch:
     int columns;     // (sequence, head, split)s side by side in an XCD (0: runs of workgroups)
     int64_t grid;
 };
 
 hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s);
+// the other forms' instances (m3_kv_attend_view.hip, m3_kv_attend_parts.hip, m3_kv_attend_tile_view.hip)
+hipError_t launch_rows_view(const AttendDev& d, m3_dtype io, hipStream_t s);
+hipError_t launch_rows_parts(const AttendDev& d, m3_dtype io, hipStream_t s);
+hipError_t launch_attend_tile_view(const AttendDev& d, m3_dtype io, hipStream_t s);
+// Joins a prefix's parts with those of the sequences' own keys. splits_a: as many of the prefix
+// lie by [split][token][head]; 0: they are of even shares too.
+hipError_t launch_merge(const AttendDev& d, int splits_a, m3_dtype io, hipStream_t s);
 
 namespace {
 
@@ -62,16 +80,10 @@ __device__ __forceinline__ int64_t pair_at(const AttendDev& a, int64_t i, int64_
     return a.packed ? first_unit(a.b, i, a.group, a.packed, 1) + rt : i * a.row_tiles + rt;
 }
 
-// Kernels come in two forms: VIEW, for calls with sinks or prefixes, and without.
-
-// The pages that sequence i holds with others: its first `count`, named by `pages`.
-struct Prefix {
-    const int32_t* pages;
-    int count;
-};
-__device__ __forceinline__ Prefix prefix_of(const AttendDev& a, int64_t i) {
+// The group of sequence i (-1: none), and the pages that its sequences hold together.
+__device__ __forceinline__ int64_t group_of(const AttendDev& a, int64_t i) {
     const m3_kv_view& v = a.view;
-    if (v.groups == 0) return Prefix{nullptr, 0};
+    if (v.groups == 0) return -1;
     int64_t g = 0;
     if (v.group_start) {  // the last group that begins at or before i
         for (int64_t hi = v.groups - 1; g < hi;) {
@@ -79,16 +91,88 @@ __device__ __forceinline__ Prefix prefix_of(const AttendDev& a, int64_t i) {
             if (v.group_start[mid] <= i) g = mid;
             else hi = mid - 1;
         }
-        if (i < v.group_start[g] || i >= v.group_start[g + 1]) return Prefix{nullptr, 0};
+        if (i < v.group_start[g] || i >= v.group_start[g + 1]) return -1;
     }
+    return g;
+}
+struct Prefix {
+    const int32_t* pages;
+    int count;
+};
+__device__ __forceinline__ Prefix prefix_at(const AttendDev& a, int64_t g) {
+    const m3_kv_view& v = a.view;
+    if (g < 0) return Prefix{nullptr, 0};
     return Prefix{v.prefix_pages + g * v.max_prefix, min(max(v.prefix_count[g], 0), int(v.max_prefix))};
+}
+__device__ __forceinline__ Prefix prefix_of(const AttendDev& a, int64_t i) { return prefix_at(a, group_of(a, i)); }
+
+// A group's sequences and rows.
+__device__ __forceinline__ int64_t sequence_at(const AttendDev& a, int64_t g) {  // its first (of g = groups: the end)
+    const m3_kv_view& v = a.view;
+    return v.group_start ? min(max(int64_t(v.group_start[g]), int64_t(0)), a.b.batch) : g * a.b.batch;
+}
+__device__ __forceinline__ int64_t row_at(const AttendDev& a, int64_t i) {  // a sequence's first row
+    return a.b.cu_q ? min(max(int64_t(a.b.cu_q[i]), int64_t(0)), a.b.tokens) : i;
+}
+struct Group {
+    int64_t first, last;  // its sequences (last: one beyond)
+    int64_t row0;
+    int n;                // rows
+    int held;             // keys of its prefix
+    Prefix pre;
+};
+__device__ __forceinline__ Group group_at(const AttendDev& a, int64_t g) {
+    Group r;
+    r.first = sequence_at(a, g);
+    r.last = max(sequence_at(a, g + 1), r.first);
+    r.row0 = row_at(a, r.first);
+    r.n = int(max(row_at(a, r.last) - r.row0, int64_t(0)));
+    r.pre = prefix_at(a, g);
+    r.held = int(min(int64_t(r.pre.count) * a.c.page_size, a.b.max_kv));
+    return r;
+}
+// Keys of its group's prefix that row `tok` sees: all, but where its sequence ends or (causal) it
+// lies within.
+__device__ __forceinline__ int row_limit(const AttendDev& a, const Group& gr, int64_t tok) {
+    int64_t i = tok;
+    if (a.b.cu_q) {  // the last sequence that begins at or before the row
+        i = gr.first;
+        for (int64_t hi = gr.last - 1; i < hi;) {
+            const int64_t mid = (i + hi + 1) / 2;
+            if (a.b.cu_q[mid] <= tok) i = mid;
+            else hi = mid - 1;
+        }
+    }
+    const Seq s = seq_of(a.b, i);
+    const int64_t t = tok - s.row0;
+    if (t < 0 || t >= s.n) return 0;
+    int64_t hi = min(gr.held, s.held);
+    if (a.causal) hi = min(hi, s.base + t + 1);
+    return int(max(hi, int64_t(0)));
+}
+// The group and row tile of pair e, and back (as pair_of and pair_at).
+__device__ __forceinline__ int64_t group_unit(const AttendDev& a, int64_t g) {
+    return (row_at(a, sequence_at(a, g)) * a.group >> a.packed_a) + g;
+}
+__device__ __forceinline__ Unit group_pair_of(const AttendDev& a, int e) {
+    if (!a.packed_a) return Unit{unsigned(e) / unsigned(a.row_tiles_a), unsigned(e) % unsigned(a.row_tiles_a)};
+    int64_t g = 0;
+    for (int64_t hi = a.view.groups - 1; g < hi;) {
+        const int64_t mid = (g + hi + 1) / 2;
+        if (group_unit(a, mid) <= e) g = mid;
+        else hi = mid - 1;
+    }
+    return Unit{g, e - group_unit(a, g)};
+}
+__device__ __forceinline__ int64_t group_pair_at(const AttendDev& a, int64_t g, int64_t rt) {
+    return a.packed_a ? group_unit(a, g) + rt : g * a.row_tiles_a + rt;
 }
 
 // Tiles of 64 keys that rows r0 .. r0 + rows - 1 of a sequence can see: number t of lo .. hi
-// - 1 is tile t, under sinks tile t + skip from the first that the window shows on.
+// - 1 is tile t; in the kView form tile t + skip from the first that the window shows on.
 struct Span {
     int64_t lo, hi;
-    int sinks, skip;  // (VIEW) tiles of the sinks alone, tiles between them and the window's
+    int sinks, skip;  // (kView) tiles of the sinks alone, tiles between them and the window's
 };
 // Keeps what is computed from a register after this point, where the compiler would form it
 // early and hold it.
@@ -96,19 +180,20 @@ __device__ __forceinline__ unsigned here(unsigned w) {
     asm volatile("" : "+v"(w));
     return w;
 }
-template <bool VIEW>
+template <Form F>
 __device__ __forceinline__ int tile_at(const Span& sp, int t) {
-    if constexpr (VIEW) return t < sp.sinks ? t : t + sp.skip;
+    if constexpr (F == kView) return t < sp.sinks ? t : t + sp.skip;
     else return t;
 }
-template <bool VIEW>
-__device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0) {
+template <Form F>
+__device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0, int own = 0) {
     const int r1 = min(r0 + a.rows, s.n * a.group) - 1;
     const int64_t base = s.base;
     int64_t hi = min(int64_t(s.held), a.b.max_kv), lo = 0;
     if (a.causal) hi = min(hi, base + r1 / a.group + 1);
     if (a.window) lo = max(int64_t(0), base + r0 / a.group - a.window + 1);
-    if constexpr (VIEW) {
+    if constexpr (F == kParts) lo = own;  // (no window there; own: the sequence's first key of its own)
+    if constexpr (F == kView) {
         const int64_t first = min(min(a.view.sinks, lo), hi);  // keys that only sinks show
         if (hi <= lo && first <= 0) return Span{0, 0, 0, 0};
         const int sinks = int((max(first, int64_t(0)) + kTile - 1) / kTile);
@@ -128,9 +213,12 @@ __device__ __forceinline__ Span span_of(const AttendDev& a, const Seq& s, int r0
 struct Cut {
     int per, pieces;
 };
-__device__ __forceinline__ Cut cut_of(const AttendDev& a, const Span& sp) {
-    const int n = int(sp.hi - sp.lo), per = max((n + a.splits - 1) / a.splits, kPieceTiles);
+__device__ __forceinline__ Cut cut_of(int n, int splits, int least) {
+    const int per = max((n + splits - 1) / splits, least);
     return Cut{per, max((n + per - 1) / per, 1)};
+}
+__device__ __forceinline__ Cut cut_of(const AttendDev& a, const Span& sp) {
+    return cut_of(int(sp.hi - sp.lo), a.splits, kPieceTiles);
 }
 
 // 8 entries of a query row as MFMA operands: one bf16 part, or three that add

@@ -183,8 +183,8 @@ namespace m3 {
 // sequences first, a column's in one XCD). Under a bound of all rows instead of the
 // longest's: 128 single tokens over 2100 57 us and 49 (187 by the bound alone), 64 prompts
 // of 300 113 and 100 (402), 4 prompts of 2048 108 and 107 (142 with the pairs packed).
-AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
-                       m3_dtype io) {
+static AttendPlan one_pass_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
+                                m3_dtype io) {
     AttendPlan p{};
     const int32_t causal = view.causal;
     const int64_t window = view.window;
@@ -227,6 +227,81 @@ AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_v
     p.ml_off = p.o_off + parts * size_t(c.headdim) * 4;
     p.total = parts ? p.ml_off + parts * 8 : 0;
     return p;
+}
+
+// The prefix and the sequences' own keys as parts: `p` is the plan of one pass, for few rows a
+// sequence.
+static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view,
+                             int32_t q_heads, m3_dtype io) {
+    PrefixPlan f{};
+    const int64_t group = q_heads / c.heads, groups = view.groups;
+    const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
+    const int64_t tiles = (b.max_kv + 63) / 64, pre = (std::min(b.max_kv, view.max_prefix * c.page_size) + 63) / 64;
+    // a group's rows: all where there is one, else four times the mean at most
+    const int64_t most = view.group_start ? std::min(b.tokens, 4 * ((b.tokens + groups - 1) / groups)) : b.tokens;
+    auto count = [&](int64_t rows) {
+        f.rows = int32_t(rows);
+        f.row_tiles = std::max<int64_t>(1, (b.tokens * group + rows - 1) / rows);
+        const int64_t packed = b.tokens * group / rows + groups;
+        f.packed = view.group_start && 2 * packed <= groups * f.row_tiles;
+        return f.packed ? packed : groups * f.row_tiles;
+    };
+    auto own_items = [&]() { return p.packed ? b.tokens * group / p.rows + b.batch : b.batch * p.row_tiles; };
+    f.tile = most * group > (io == M3_BF16 && width < 2 ? 64 : 32);
+    const int64_t full = width == 2 ? 256 : 512, every = b.tokens * q_heads;
+    if (!f.tile) {
+        if (most * group > 16 && width < 2 && p.rows == 16) {  // as many rows a tile as the groups have
+            p.rows = 32;
+            p.row_tiles = std::max<int64_t>(1, (b.max_q * group + 31) / 32);
+            p.packed = b.cu_q && 2 * (b.tokens * group / 32 + b.batch) <= b.batch * p.row_tiles;
+        }
+        const int64_t a = count(p.rows), all = a + own_items();
+        if (all > kAttendItems || all * (tiles + 4) > INT32_MAX) {
+            f.tile = true;
+        } else {
+            f.items = int32_t(a);
+            p.items = int32_t(all);
+            const int64_t four = c.heads * (std::min(a, b.tokens * group / p.rows + groups) * ((pre + 3) / 4) + own_items() * ((tiles + 3) / 4));
+            p.blocks = std::max<int64_t>(1, std::min(full, four));
+        }
+    }
+    size_t rows = 0;
+    if (f.tile) {
+        const int64_t items = count((io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width]);
+        const int64_t busy = std::max<int64_t>(1, std::min(items, b.tokens * group / f.rows + groups) * c.heads);
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / busy, pre / kPrefixPiece));
+        f.split_tiles = std::max<int64_t>(1, (pre + want - 1) / want);
+        f.splits = int32_t(std::max<int64_t>(1, (pre + f.split_tiles - 1) / f.split_tiles));
+        f.blocks = items * c.heads * f.splits;
+        rows = size_t(f.splits) * size_t(every);
+        const int64_t own = own_items();
+        p.items = tiles > 16 && own * c.heads < full && own <= kAttendItems && own * (tiles + 4) <= INT32_MAX ? int32_t(own) : 0;
+        p.blocks = p.items ? std::min<int64_t>(full, own * c.heads * ((tiles + 3) / 4)) : std::max<int64_t>(1, own * c.heads);
+    }
+    f.slots = rows;
+    if (p.items) rows += size_t(2 * p.blocks) * size_t(p.rows);
+    f.solo = rows;
+    if (!f.tile) rows += size_t(every);
+    f.solo_own = rows;
+    rows += size_t(every);
+    p.parts = true;
+    p.prefix = f;
+    p.o_off = p.items ? (size_t(p.items + 2) * 4 + 255) / 256 * 256 : 0;
+    p.ml_off = p.o_off + rows * size_t(c.headdim) * 4;
+    p.total = p.ml_off + rows * 8;
+    return p;
+}
+
+// Parts where they save enough: without them every sequence reads its group's prefix (from L2 or
+// the last cache level, mostly), for rows that the products hardly notice; with them there are
+// the parts to write and a launch to join them.
+constexpr int64_t kPartsBytes = int64_t(4) << 20;
+AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
+                       m3_dtype io) {
+    const AttendPlan p = one_pass_plan(c, b, view, q_heads, io);
+    if (view.groups == 0 || view.window > 0 || p.tile || b.batch <= view.groups) return p;
+    const int64_t prefix = std::min(b.max_kv, view.max_prefix * c.page_size) * 2 * c.heads * c.headdim;
+    return (b.batch - view.groups) * double(prefix) < double(kPartsBytes) ? p : parts_plan(p, c, b, view, q_heads, io);
 }
 
 }  // namespace m3
@@ -419,7 +494,7 @@ m3_status m3_kv_attend_view(const m3_kv_cache* cache, const m3_kv_batch* batch, 
             return set_error(M3_EWORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, a.plan.total);
         if (!aligned(workspace, 16)) return set_error(M3_EALIGN, "workspace is not 16-byte aligned");
     }
-    if (a.plan.blocks > INT32_MAX - 7) return set_error(M3_EUNSUPPORTED, "too many workgroups");
+    if (a.plan.blocks > INT32_MAX - 7 || a.plan.prefix.blocks > INT32_MAX - 7) return set_error(M3_EUNSUPPORTED, "too many workgroups");
     const hipError_t e = m3::launch_kv_attend(a);
     if (e != hipSuccess) return set_error(M3_EHIP, "attend launch failed: %s", hipGetErrorString(e));
     return M3_OK;

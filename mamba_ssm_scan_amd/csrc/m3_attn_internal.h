@@ -64,6 +64,16 @@ hipError_t launch_kv_read(const ReadArgs& a);
 // for many rows: `splits` workgroups along a row tile's keys, at most `split_tiles`
 // tiles each (cut_of). The kernel for few: `items` > 0 gives every workgroup an even share of all
 // tiles, 0 a row tile each.
+struct PrefixPlan {       // of the prefix, where it is a part of its own
+    bool tile;            // its own launch of the kernel for many rows; else items of the other's launch
+    int32_t rows;
+    int64_t row_tiles;    // of a group
+    bool packed;
+    int32_t items;        // (group, row tile) pairs
+    int32_t splits;
+    int64_t split_tiles, blocks;
+    size_t slots, solo, solo_own;  // where parts lie, in rows: of even shares, of a run that one workgroup holds
+};
 struct AttendPlan {
     bool tile;            // the kernel for many rows a sequence
     int32_t rows;         // rows of a tile
@@ -74,7 +84,10 @@ struct AttendPlan {
     bool packed;          // they follow one another (unit_of), as max_q is loose
     int64_t blocks;       // workgroups
     size_t o_off, ml_off, total;  // workspace: the shares (even ones), sums of parts, (unit, sum) pairs
+    bool parts;           // the prefix and the sequences' own keys as parts
+    PrefixPlan prefix;
 };
+constexpr int32_t kPrefixPiece = 4;     // least tiles of a piece of a prefix (many rows)
 constexpr int32_t kPieceTiles = 8;      // least tiles of a piece, where a row tile's keys are cut (many rows)
 constexpr int32_t kAttendItems = 2048;  // most items whose first tiles a workgroup holds
 // Rows of a workgroup of the kernel for many rows, by headdim (<= 64, <= 128, <= 256);
