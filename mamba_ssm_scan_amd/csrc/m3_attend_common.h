@@ -38,7 +38,7 @@ struct AttendDev {
     m3_kv_view view;
     // The kParts form: the groups' (group, row tile) pairs come before the sequences' among the
     // items, numbered by their own row tiles; where parts lie (in rows of part_o, part_ml).
-    int items_a, packed_a;
+    int items_a, packed_a, splits_a;  // splits_a: the prefix's parts by [split][token][head]; 0: even shares too
     int64_t row_tiles_a, slots, solo_a, solo_b;
     // of the tile kernel's launch:
     int columns;     // (sequence, head, split)s side by side in an XCD (0: runs of workgroups)
@@ -50,9 +50,9 @@ hipError_t launch_attend_tile(const AttendDev& d, m3_dtype io, hipStream_t s);
 hipError_t launch_rows_view(const AttendDev& d, m3_dtype io, hipStream_t s);
 hipError_t launch_rows_parts(const AttendDev& d, m3_dtype io, hipStream_t s);
 hipError_t launch_attend_tile_view(const AttendDev& d, m3_dtype io, hipStream_t s);
-// Joins a prefix's parts with those of the sequences' own keys. splits_a: as many of the prefix
-// lie by [split][token][head]; 0: they are of even shares too.
-hipError_t launch_merge(const AttendDev& d, int splits_a, m3_dtype io, hipStream_t s);
+// Joins a prefix's parts with those of the sequences' own keys, where both are of even shares or
+// the own ones are.
+hipError_t launch_merge(const AttendDev& d, m3_dtype io, hipStream_t s);
 
 namespace {
 

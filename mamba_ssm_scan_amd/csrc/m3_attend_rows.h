@@ -104,7 +104,7 @@ __device__ __forceinline__ void zero_rows(const AttendDev& a, const int* first) 
 // Waves a SIMD: what the registers of each case allow without spilling in its loop.
 template <typename T, int DP, int QT, bool FULL, bool EVEN, Form F>
 constexpr int kSimdWaves = DP == 256 || (sizeof(T) == 4 && DP * QT > 128)            ? 1
-                           : F != kPlain && DP * QT > 128 && (EVEN || !FULL)         ? 1
+                           : F == kView && DP * QT > 128 && (EVEN || !FULL)          ? 1
                            : sizeof(T) == 4 || QT == 2                               ? 2
                            : DP == 64                                                ? 4
                            : EVEN || F != kPlain                                     ? 2
@@ -172,13 +172,16 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, FULL, EVEN, F>)
         }
         Seq sq;
         Group gr{};
-        int own = 0;  // (kParts) the first key of the sequence's own
+        int own = 0, pieces = 0;  // (kParts) the first key of the sequence's own
         if (F == kParts && shared) {
             gr = group_at(a, i);
             sq = Seq{gr.row0, gr.n, gr.held, 0};
         } else {
             sq = seq_of(a.b, i);
             if constexpr (F == kParts) own = own_key(a, i);
+            // pieces of the prefix (the kernel for many rows cut them)
+            if (F == kParts && !EVEN && own > 0)
+                pieces = cut_of(int((min(int64_t(own), a.b.max_kv) + kTile - 1) / kTile), a.splits_a, kPrefixPiece).pieces;
         }
         const int rows = sq.n * a.group;
         if (rt < 0 || rt * a.rows >= rows) break;  // (without shares only)
@@ -459,6 +462,33 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, FULL, EVEN, F>)
                 if (direct) {
                     store8<true>(static_cast<T*>(a.out) + at * D + d, v);
                     if (a.lse && d == 0) a.lse[at] = l == 0.f ? -INFINITY : mm * kLn2 + __logf(l);
+                } else if (F == kParts && !EVEN) {
+                    // the prefix's parts, written by the launch before, joined with the row's own
+                    const int64_t every = a.b.tokens * a.q_heads;
+                    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + at;
+                    const float* po = a.part_o + at * D + d;
+                    float top = mm;
+#pragma unroll 8
+                    for (int p = 0; p < pieces; ++p) top = fmaxf(top, ml[p * every].x);
+                    const float f0 = mm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mm - top);
+                    float sum_l = mm == -INFINITY ? l : l * f0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= f0;
+#pragma unroll 8
+                    for (int p = 0; p < pieces; ++p) {
+                        const float2 w = ml[p * every];
+                        const float f = w.x == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(w.x - top);
+                        sum_l += w.x == -INFINITY ? w.y : w.y * f;
+                        float u[8];
+                        load8<true>(po + p * every * D, u);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = __builtin_fmaf(u[k], f, v[k]);
+                    }
+                    const float r = sum_l == 0.f ? 0.f : 1.f / sum_l;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] *= r;
+                    store8<true>(static_cast<T*>(a.out) + at * D + d, v);
+                    if (a.lse && d == 0) a.lse[at] = sum_l == 0.f ? -INFINITY : top * kLn2 + __logf(sum_l);
                 } else {
                     const int64_t pt = F == kParts && whole ? (shared ? a.solo_a : a.solo_b) + at
                                                             : (F == kParts ? a.slots : 0) + int64_t(slot) * a.rows + 16 * qt + q;
@@ -483,13 +513,19 @@ void launch_rows(const AttendDev& d, hipStream_t s) {
         d.D == DP ? launch(attend_rows_kernel<T, FP8, DP, QT, true, false, F>)
                   : launch(attend_rows_kernel<T, FP8, DP, QT, false, false, F>);
 }
-// Rows of a tile: 16 or (headdim 128 at most) 32.
+// Rows of a tile: 16 or (headdim 128 at most, not kParts) 32.
 template <typename T, bool FP8, Form F>
 hipError_t launch_rows_dim(const AttendDev& d, hipStream_t s) {
-    const bool one = d.rows == 16;
-    if (d.D <= 64) one ? launch_rows<T, FP8, 64, 1, F>(d, s) : launch_rows<T, FP8, 64, 2, F>(d, s);
-    else if (d.D <= 128) one ? launch_rows<T, FP8, 128, 1, F>(d, s) : launch_rows<T, FP8, 128, 2, F>(d, s);
-    else launch_rows<T, FP8, 256, 1, F>(d, s);
+    if constexpr (F == kParts) {
+        if (d.D <= 64) launch_rows<T, FP8, 64, 1, F>(d, s);
+        else if (d.D <= 128) launch_rows<T, FP8, 128, 1, F>(d, s);
+        else launch_rows<T, FP8, 256, 1, F>(d, s);
+    } else {
+        const bool one = d.rows == 16;
+        if (d.D <= 64) one ? launch_rows<T, FP8, 64, 1, F>(d, s) : launch_rows<T, FP8, 64, 2, F>(d, s);
+        else if (d.D <= 128) one ? launch_rows<T, FP8, 128, 1, F>(d, s) : launch_rows<T, FP8, 128, 2, F>(d, s);
+        else launch_rows<T, FP8, 256, 1, F>(d, s);
+    }
     return hipGetLastError();
 }
 template <Form F>

@@ -10,7 +10,7 @@ namespace m3 {
 namespace {
 
 template <typename T, bool FP8, int DP, int QT, int NW, Form F>
-__global__ __launch_bounds__(64 * NW, DP == 64 && !(F != kPlain && QT == 2) ? 3 : 2) void attend_tile_kernel(AttendDev a) {
+__global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 : 2) void attend_tile_kernel(AttendDev a) {
     constexpr int NP = Parts<T>::kN, NV = Parts<T>::kV;
     constexpr int KM = DP / 32;          // MFMA steps of a score (32 entries each)
     constexpr int DT = DP / 16;
@@ -83,6 +83,123 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F != kPlain && QT == 2) ? 3 
     const int key = lane & 15;  // (16 keys in turn: a group of 16 lanes writes 16 bank columns)
     auto kc = [&](int j) { return (lane >> 4) + (64 * wave + NT * j) % DP / 16; };
 
+    // what a wave brings of a tile: piece p = 64 wave + lane + NT j of K (16 codes of a
+    // key) and of V (16 tokens of entry p % DP), of block p / DP, so that a wave's
+    // pieces of one j lie in one block and their page is looked up once, in scalars
+    const int32_t* pages = F == kParts ? gr.pre.pages : a.b.pages + i * a.b.max_pages;
+    const int swave = __builtin_amdgcn_readfirstlane(wave);
+    struct Raw {
+        u32x4 k[PC], v[PC];
+        float ks[PC], vs[PC];
+        bool there[PC];  // whether V's block (and its scales) is held
+    };
+    struct Pages {
+        int p[PC];   // page number of this wave's blocks of a tile (-1: none)
+    };
+    // (kView) keys that sinks show, the first block that the window does, and the shared pages
+    const int sinks = F == kView ? int(a.view.sinks) : 0, sink_blocks = (sinks + 15) / 16;
+    const int win_block = F == kView && a.window ? int(max(base + r0 / a.group - a.window + 1, int64_t(0)) / 16) : 0;
+    const Prefix pre = F == kView ? prefix_of(a, i) : Prefix{nullptr, 0};
+    auto find = [&](int tile) {
+        Pages r;
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int blk = tile_at<F>(sp, tile) * 4 + (64 * swave + NT * j) / DP, pg = blk >> a.shift;
+            r.p[j] = -1;
+            if (F == kView && blk < win_block && blk >= sink_blocks) continue;
+            // (forms other than kPlain: max_kv ends in the table)
+            if (tile < t1 && blk < held_blocks && (F != kPlain || pg < a.b.max_pages))
+                r.p[j] = F == kView && pg < pre.count ? pre.pages[pg] : pages[pg];
+        }
+        return r;
+    };
+    auto block = [&](int tile, const Pages& pg, int j) -> int64_t {
+        const int blk = tile_at<F>(sp, tile) * 4 + (64 * swave + NT * j) / DP;
+        const int64_t page = __builtin_amdgcn_readfirstlane(pg.p[j]);
+        if (page < 0 || page >= a.c.num_pages) return -1;
+        return ((page * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
+    };
+    auto fetch_k = [&](Raw& r, int tile, const Pages& pg) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int64_t at = block(tile, pg, j);
+            r.k[j] = u32x4{0, 0, 0, 0};
+            if (at >= 0 && 16 * kc(j) < D)
+                r.k[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.k) + at * 16 * D + key * D + 16 * kc(j));
+        }
+    };
+    auto fetch_v = [&](Raw& r, int tile, const Pages& pg) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int64_t at = block(tile, pg, j);
+            const int d = (64 * swave + NT * j) % DP + lane;
+            r.v[j] = u32x4{0, 0, 0, 0};
+            r.ks[j] = r.vs[j] = 0.f;
+            r.there[j] = at >= 0;
+            if (at >= 0) {
+                if (d < D) r.v[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.v) + at * 16 * D + d * 16);
+                r.ks[j] = a.c.k_scale[at];
+                r.vs[j] = a.c.v_scale[at];
+            }
+        }
+    };
+    auto stage_k = [&](const Raw& raw, int buf) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int blk = (64 * swave + NT * j) / DP;
+            // key 16 blk + 4 t + e is row 4 blk + e of score tile t; its place among a
+            // piece's 16 rows is turned by 4 t, so that a wave's writes take all banks
+            const int t = key >> 2, r = (4 * blk + (key & 3) + 4 * t) & 15;
+            const int cg = kc(j) / (KM / 2), cj = kc(j) % (KM / 2);
+            char* kp = lds + buf * KB + ((t * KM + 2 * cj) * 64 + cg * 16 + r) * 16;
+            *reinterpret_cast<u32x4*>(kp) = to_bf16<FP8>(raw.k[j][0], raw.k[j][1]);
+            *reinterpret_cast<u32x4*>(kp + 1024) = to_bf16<FP8>(raw.k[j][2], raw.k[j][3]);
+        }
+    };
+    auto stage_v = [&](const Raw& raw, int tile, int buf) {
+#pragma unroll
+        for (int j = 0; j < PC; ++j) {
+            const int p0 = 64 * swave + NT * j;
+            const int blk = p0 / DP, d = p0 % DP + lane;
+            u32x4 v = raw.v[j];
+            const VScale vs = v_scale(raw.vs[j]);
+            if (vs.none) v = u32x4{0, 0, 0, 0};
+            const int k0 = tile_at<F>(sp, tile) * kTile;
+            if (k0 + kTile > held) {  // codes of slots that hold no token may be anything
+                const int nv = min(max(held - (k0 + 16 * blk), 0), 16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int n = min(max(nv - 4 * w, 0), 4);
+                    v[w] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
+                }
+            }
+            char* vp = lds + (2 + buf) * KB + ((d / 16) * 2 * 64 + blk * 16 + d % 16) * 16;
+            *reinterpret_cast<u32x4*>(vp) = v_operand<FP8, NV>(v[0], v[1]);
+            *reinterpret_cast<u32x4*>(vp + 1024) = v_operand<FP8, NV>(v[2], v[3]);
+            if (p0 % DP == 0 && lane == 0) {
+                *reinterpret_cast<floatx4*>(sc_lds[buf][blk]) =
+                    floatx4{raw.ks[j] * a.scale2, vs.log2, vs.inv, raw.there[j] ? 1.f : 0.f};
+            }
+        }
+    };
+    // The forms other than kPlain have short runs of keys (a window's, a piece of a prefix), and
+    // a wave's waits weigh more: page numbers and the first loads go out together and before
+    // the rows' own, and (kDeep, where registers allow) each tile's loads a turn earlier. 128
+    // steps behind 8192 tokens: FIGURE_DEEP.
+    constexpr bool kDeep = F != kPlain && QT == 1 && !(DP == 256 && NP == 3);
+    Raw ra, rb;
+    Pages pgv{}, pgk{};
+    if constexpr (F != kPlain) {
+        if (t0 < t1) {
+            const Pages first = find(t0);
+            pgv = find(t0 + 1);
+            pgk = find(t0 + 2);
+            fetch_k(ra, t0, first);
+            fetch_v(ra, t0, first);
+            if constexpr (kAhead) fetch_k(rb, t0 + 1, pgv);
+        }
+    }
+
     // this wave's rows
     u32x4 qf[QT][KM][NP];
     int klo[QT], khi[QT];
@@ -141,103 +258,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F != kPlain && QT == 2) ? 3 
         for (int d = 0; d < DT; ++d) o[qt][d] = floatx4{0, 0, 0, 0};
     }
 
-    // what a wave brings of a tile: piece p = 64 wave + lane + NT j of K (16 codes of a
-    // key) and of V (16 tokens of entry p % DP), of block p / DP, so that a wave's
-    // pieces of one j lie in one block and their page is looked up once, in scalars
-    const int32_t* pages = F == kParts ? gr.pre.pages : a.b.pages + i * a.b.max_pages;
-    const int swave = __builtin_amdgcn_readfirstlane(wave);
-    u32x4 rk[PC], rv[PC];
-    float rks[PC], rvs[PC];
-    bool there[PC];  // whether V's block (and its scales) is held
-    struct Pages {
-        int p[PC];   // page number of this wave's blocks of a tile (-1: none)
-    };
-    // (kView) keys that sinks show, the first block that the window does, and the shared pages
-    const int sinks = F == kView ? int(a.view.sinks) : 0, sink_blocks = (sinks + 15) / 16;
-    const int win_block = F == kView && a.window ? int(max(base + r0 / a.group - a.window + 1, int64_t(0)) / 16) : 0;
-    const Prefix pre = F == kView ? prefix_of(a, i) : Prefix{nullptr, 0};
-    auto find = [&](int tile) {
-        Pages r;
-#pragma unroll
-        for (int j = 0; j < PC; ++j) {
-            const int blk = tile_at<F>(sp, tile) * 4 + (64 * swave + NT * j) / DP, pg = blk >> a.shift;
-            r.p[j] = -1;
-            if (F == kView && blk < win_block && blk >= sink_blocks) continue;
-            // (forms other than kPlain: max_kv ends in the table)
-            if (tile < t1 && blk < held_blocks && (F != kPlain || pg < a.b.max_pages))
-                r.p[j] = F == kView && pg < pre.count ? pre.pages[pg] : pages[pg];
-        }
-        return r;
-    };
-    auto block = [&](int tile, const Pages& pg, int j) -> int64_t {
-        const int blk = tile_at<F>(sp, tile) * 4 + (64 * swave + NT * j) / DP;
-        const int64_t page = __builtin_amdgcn_readfirstlane(pg.p[j]);
-        if (page < 0 || page >= a.c.num_pages) return -1;
-        return ((page * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
-    };
-    auto fetch_k = [&](int tile, const Pages& pg) {
-#pragma unroll
-        for (int j = 0; j < PC; ++j) {
-            const int64_t at = block(tile, pg, j);
-            rk[j] = u32x4{0, 0, 0, 0};
-            if (at >= 0 && 16 * kc(j) < D)
-                rk[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.k) + at * 16 * D + key * D + 16 * kc(j));
-        }
-    };
-    auto fetch_v = [&](int tile, const Pages& pg) {
-#pragma unroll
-        for (int j = 0; j < PC; ++j) {
-            const int64_t at = block(tile, pg, j);
-            const int d = (64 * swave + NT * j) % DP + lane;
-            rv[j] = u32x4{0, 0, 0, 0};
-            rks[j] = rvs[j] = 0.f;
-            there[j] = at >= 0;
-            if (at >= 0) {
-                if (d < D) rv[j] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.c.v) + at * 16 * D + d * 16);
-                rks[j] = a.c.k_scale[at];
-                rvs[j] = a.c.v_scale[at];
-            }
-        }
-    };
-    auto stage_k = [&](int buf) {
-#pragma unroll
-        for (int j = 0; j < PC; ++j) {
-            const int blk = (64 * swave + NT * j) / DP;
-            // key 16 blk + 4 t + e is row 4 blk + e of score tile t; its place among a
-            // piece's 16 rows is turned by 4 t, so that a wave's writes take all banks
-            const int t = key >> 2, r = (4 * blk + (key & 3) + 4 * t) & 15;
-            const int cg = kc(j) / (KM / 2), cj = kc(j) % (KM / 2);
-            char* kp = lds + buf * KB + ((t * KM + 2 * cj) * 64 + cg * 16 + r) * 16;
-            *reinterpret_cast<u32x4*>(kp) = to_bf16<FP8>(rk[j][0], rk[j][1]);
-            *reinterpret_cast<u32x4*>(kp + 1024) = to_bf16<FP8>(rk[j][2], rk[j][3]);
-        }
-    };
-    auto stage_v = [&](int tile, int buf) {
-#pragma unroll
-        for (int j = 0; j < PC; ++j) {
-            const int p0 = 64 * swave + NT * j;
-            const int blk = p0 / DP, d = p0 % DP + lane;
-            u32x4 v = rv[j];
-            const VScale vs = v_scale(rvs[j]);
-            if (vs.none) v = u32x4{0, 0, 0, 0};
-            const int k0 = tile_at<F>(sp, tile) * kTile;
-            if (k0 + kTile > held) {  // codes of slots that hold no token may be anything
-                const int nv = min(max(held - (k0 + 16 * blk), 0), 16);
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const int n = min(max(nv - 4 * w, 0), 4);
-                    v[w] &= n == 4 ? ~0u : (1u << (8 * n)) - 1u;
-                }
-            }
-            char* vp = lds + (2 + buf) * KB + ((d / 16) * 2 * 64 + blk * 16 + d % 16) * 16;
-            *reinterpret_cast<u32x4*>(vp) = v_operand<FP8, NV>(v[0], v[1]);
-            *reinterpret_cast<u32x4*>(vp + 1024) = v_operand<FP8, NV>(v[2], v[3]);
-            if (p0 % DP == 0 && lane == 0) {
-                *reinterpret_cast<floatx4*>(sc_lds[buf][blk]) =
-                    floatx4{rks[j] * a.scale2, vs.log2, vs.inv, there[j] ? 1.f : 0.f};
-            }
-        }
-    };
     // piece m of score tile t of a K image, and the scores' products with it
     int kt[4];
 #pragma unroll
@@ -270,32 +290,46 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F != kPlain && QT == 2) ? 3 
     // without the second set of scores do better (K and V of n + 1 are converted in turn n).
     // So do the two that headdim 256 leaves (one prompt of 2048, 16 heads over 4: bf16 103 us
     // and 108 with the second set, fp32 164 and 203, where it spills).
-    Pages pgv{}, pgk{};
     if (t0 < t1) {
-        pgk = find(t0);
-        fetch_k(t0, pgk);
-        fetch_v(t0, pgk);
-        pgv = find(t0 + 1);
-        stage_k(0);
-        stage_v(t0, 0);
+        if constexpr (F == kPlain) {
+            pgk = find(t0);
+            fetch_k(ra, t0, pgk);
+            fetch_v(ra, t0, pgk);
+            pgv = find(t0 + 1);
+        }
+        stage_k(ra, 0);
+        stage_v(ra, t0, 0);
         if constexpr (kAhead) {
-            fetch_k(t0 + 1, pgv);
-            pgk = find(t0 + 2);
-            stage_k(1);
+            if constexpr (F == kPlain) {
+                fetch_k(ra, t0 + 1, pgv);
+                pgk = find(t0 + 2);
+                stage_k(ra, 1);
+            } else {
+                stage_k(rb, 1);
+            }
+        }
+        if constexpr (kDeep) {  // what turn t0 puts into LDS
+            fetch_v(ra, t0 + 1, pgv);
+            fetch_k(ra, t0 + (kAhead ? 2 : 1), kAhead ? pgk : pgv);
+            pgv = pgk;
+            pgk = find(t0 + 3);
+        }
+        if constexpr (kAhead) {
             __syncthreads();
             if (seen(t0)) scores(0, s);
         }
         __syncthreads();
     }
     float inv_top = -INFINITY;  // scales of a 1 / vs above it ask for the maxima (all, until every row of the wave has a reference)
-    auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4]) {
-        fetch_v(tile + 1, pgv);  // (nothing after the last)
-        if constexpr (kAhead) {
-            fetch_k(tile + 2, pgk);
+    // `put`: what goes to LDS at the turn's end, `get`: what is requested at its start
+    auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4], const Raw& put, Raw& get) {
+        constexpr int kV = kDeep ? 2 : 1, kK = kV + kAhead;  // turns until they are used (nothing after the last)
+        fetch_v(get, tile + kV, pgv);
+        fetch_k(get, tile + kK, kAhead ? pgk : pgv);
+        if constexpr (kAhead || kDeep) {
             pgv = pgk;
-            pgk = find(tile + 3);
+            pgk = find(tile + (kDeep ? 4 : 3));
         } else {
-            fetch_k(tile + 1, pgv);
             pgv = find(tile + 2);
         }
         const int k0 = tile_at<F>(sp, tile) * kTile;
@@ -382,15 +416,16 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F != kPlain && QT == 2) ? 3 
         } else if (kAhead && seen(tile + 1)) {
             scores(buf ^ 1, sn);
         }
-        stage_k(kAhead ? buf : buf ^ 1);
-        stage_v(tile + 1, buf ^ 1);
+        stage_k(put, kAhead ? buf : buf ^ 1);
+        stage_v(put, tile + 1, buf ^ 1);
         __syncthreads();
     };
+    Raw& other = kDeep ? rb : ra;
     for (int tile = t0; tile < t1; tile += 2) {
-        turn_of(tile, 0, s, sn);
+        turn_of(tile, 0, s, sn, ra, other);
         if (tile + 1 < t1) {
-            if constexpr (kAhead) turn_of(tile + 1, 1, sn, s);
-            else turn_of(tile + 1, 1, s, sn);
+            if constexpr (kAhead) turn_of(tile + 1, 1, sn, s, other, ra);
+            else turn_of(tile + 1, 1, s, sn, other, ra);
         }
     }
 

@@ -218,9 +218,10 @@ static AttendPlan one_pass_plan(const m3_kv_cache& c, const m3_kv_batch& b, cons
         p.blocks = base * p.splits;
         if (p.splits > 1) parts = size_t(p.splits) * size_t(b.tokens) * size_t(q_heads);
     } else if (const int64_t full = width == 2 ? 256 : 512;
-               tiles > 16 && base < full && items <= kAttendItems && items * tiles <= INT32_MAX) {
+               tiles > 16 && base < full && items <= kAttendItems && items * (tiles + 3) <= INT32_MAX) {
         p.items = int32_t(items);
-        p.blocks = std::min<int64_t>(full, (base * tiles + 3) / 4);
+        // (a share of 4 tiles each; under sinks or prefixes items are multiples of 4)
+        p.blocks = std::min<int64_t>(full, has_view(view) ? base * ((tiles + 3) / 4) : (base * tiles + 3) / 4);
         parts = size_t(2 * p.blocks) * size_t(p.rows);
         p.o_off = (size_t(items + 2) * 4 + 255) / 256 * 256;
     }
@@ -229,52 +230,52 @@ static AttendPlan one_pass_plan(const m3_kv_cache& c, const m3_kv_batch& b, cons
     return p;
 }
 
-// The prefix and the sequences' own keys as parts: `p` is the plan of one pass, for few rows a
-// sequence.
+// The prefix and the sequences' own keys as parts; `p` is the plan of one pass, for few rows a
+// sequence. 16 rows a tile in either case (32 leave registers for one wave a SIMD: 16 steps
+// behind 8192 tokens 27 us and 33).
+//   The groups' row tiles are items of the launch for few rows, whose waves each convert the
+// keys anew, up to 8192 (row tile, key head, tile of 64 keys) triples; beyond, the kernel for many rows
+// converts them once for 128 rows (256 where these alone fill a quarter of the chip, and parts are few)
+// in a launch of its own. Steps with 16 heads over 4 of 128: behind 8192 tokens 16 / 32 / 64 sequences 27 / 34
+// / 49 us and 32 / 38 / 46, behind 65536 4 / 8 / 16 of them 36 / 47 / 72 and 48 / 49 / 51.
 static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view,
                              int32_t q_heads, m3_dtype io) {
     PrefixPlan f{};
-    const int64_t group = q_heads / c.heads, groups = view.groups;
+    const int64_t group = q_heads / c.heads, groups = view.groups, every = b.tokens * q_heads;
     const int width = c.headdim <= 64 ? 0 : c.headdim <= 128 ? 1 : 2;
     const int64_t tiles = (b.max_kv + 63) / 64, pre = (std::min(b.max_kv, view.max_prefix * c.page_size) + 63) / 64;
-    // a group's rows: all where there is one, else four times the mean at most
-    const int64_t most = view.group_start ? std::min(b.tokens, 4 * ((b.tokens + groups - 1) / groups)) : b.tokens;
+    // (group, row tile) pairs, each group's as many as all rows fill, or one group's after the other's
+    auto busy = [&](int64_t rows) { return b.tokens * group / rows + groups; };
     auto count = [&](int64_t rows) {
         f.rows = int32_t(rows);
         f.row_tiles = std::max<int64_t>(1, (b.tokens * group + rows - 1) / rows);
-        const int64_t packed = b.tokens * group / rows + groups;
-        f.packed = view.group_start && 2 * packed <= groups * f.row_tiles;
-        return f.packed ? packed : groups * f.row_tiles;
+        f.packed = view.group_start && 2 * busy(rows) <= groups * f.row_tiles;
+        return f.packed ? busy(rows) : groups * f.row_tiles;
     };
-    auto own_items = [&]() { return p.packed ? b.tokens * group / p.rows + b.batch : b.batch * p.row_tiles; };
-    f.tile = most * group > (io == M3_BF16 && width < 2 ? 64 : 32);
-    const int64_t full = width == 2 ? 256 : 512, every = b.tokens * q_heads;
+    p.rows = 16;
+    p.row_tiles = std::max<int64_t>(1, (b.max_q * group + 15) / 16);
+    const int64_t packed = b.tokens * group / 16 + b.batch;
+    p.packed = b.cu_q && 2 * packed <= b.batch * p.row_tiles;
+    const int64_t own = p.packed ? packed : b.batch * p.row_tiles;
+    const int64_t full = width == 2 ? 256 : 512, shared = count(16);  // workgroups at once
+    f.tile = std::min(shared, busy(16)) * c.heads * pre > 8192 || shared + own > kAttendItems ||
+             (shared + own) * (tiles + 4) > INT32_MAX;
+    size_t rows = 0;  // of parts
     if (!f.tile) {
-        if (most * group > 16 && width < 2 && p.rows == 16) {  // as many rows a tile as the groups have
-            p.rows = 32;
-            p.row_tiles = std::max<int64_t>(1, (b.max_q * group + 31) / 32);
-            p.packed = b.cu_q && 2 * (b.tokens * group / 32 + b.batch) <= b.batch * p.row_tiles;
-        }
-        const int64_t a = count(p.rows), all = a + own_items();
-        if (all > kAttendItems || all * (tiles + 4) > INT32_MAX) {
-            f.tile = true;
-        } else {
-            f.items = int32_t(a);
-            p.items = int32_t(all);
-            const int64_t four = c.heads * (std::min(a, b.tokens * group / p.rows + groups) * ((pre + 3) / 4) + own_items() * ((tiles + 3) / 4));
-            p.blocks = std::max<int64_t>(1, std::min(full, four));
-        }
-    }
-    size_t rows = 0;
-    if (f.tile) {
-        const int64_t items = count((io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width]);
-        const int64_t busy = std::max<int64_t>(1, std::min(items, b.tokens * group / f.rows + groups) * c.heads);
-        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / busy, pre / kPrefixPiece));
+        f.items = int32_t(shared);
+        p.items = int32_t(shared + own);
+        const int64_t four = c.heads * (std::min(shared, busy(16)) * ((pre + 3) / 4) + own * ((tiles + 3) / 4));
+        p.blocks = std::max<int64_t>(1, std::min(full, four));
+    } else {
+        const int64_t most = (io == M3_BF16 ? kTileRowsBf16 : kTileRowsF32)[width];
+        const bool half = io == M3_BF16 && width < 2 && std::min(count(most), busy(most)) * c.heads <= 64;
+        const int64_t items = count(half ? most / 2 : most);
+        const int64_t work = std::max<int64_t>(1, std::min(items, busy(f.rows)) * c.heads);
+        const int64_t want = std::max<int64_t>(1, std::min<int64_t>(256 / work, pre / kPrefixPiece));
         f.split_tiles = std::max<int64_t>(1, (pre + want - 1) / want);
         f.splits = int32_t(std::max<int64_t>(1, (pre + f.split_tiles - 1) / f.split_tiles));
         f.blocks = items * c.heads * f.splits;
         rows = size_t(f.splits) * size_t(every);
-        const int64_t own = own_items();
         p.items = tiles > 16 && own * c.heads < full && own <= kAttendItems && own * (tiles + 4) <= INT32_MAX ? int32_t(own) : 0;
         p.blocks = p.items ? std::min<int64_t>(full, own * c.heads * ((tiles + 3) / 4)) : std::max<int64_t>(1, own * c.heads);
     }
@@ -283,7 +284,7 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
     f.solo = rows;
     if (!f.tile) rows += size_t(every);
     f.solo_own = rows;
-    rows += size_t(every);
+    if (p.items) rows += size_t(every);
     p.parts = true;
     p.prefix = f;
     p.o_off = p.items ? (size_t(p.items + 2) * 4 + 255) / 256 * 256 : 0;

@@ -180,6 +180,7 @@ hipError_t launch_kv_attend(const AttendArgs& a) {
     d.solo_a = int64_t(f.solo);
     d.solo_b = int64_t(f.solo_own);
     if (f.tile) {
+        d.splits_a = f.splits;
         AttendDev t = d;
         t.items = 0;
         t.packed = d.packed_a;
@@ -192,8 +193,8 @@ hipError_t launch_kv_attend(const AttendArgs& a) {
     } else {
         d.items_a = f.items;
     }
-    if ((e = launch_few(d, a.io, a.stream)) != hipSuccess) return e;
-    return launch_merge(d, f.tile ? f.splits : 0, a.io, a.stream);
+    if ((e = launch_few(d, a.io, a.stream)) != hipSuccess || !p.items) return e;
+    return launch_merge(d, a.io, a.stream);
 }
 
 }  // namespace m3

@@ -5,8 +5,9 @@
 // So a group's prefix is one more run of keys, whose rows are all its sequences' rows: read once
 // for as many of them as a row tile holds, where every sequence would read it for a few rows.
 // Up to 64 rows of a key head a group, the groups' row tiles and the sequences' are items of one
-// launch of the kernel for few rows, dealt out in even shares; above, the prefix goes through the kernel
-// for many rows first. The merge takes a row's parts of both in their order.
+// launch of the kernel for few rows, dealt out in even shares, and a merge takes a row's parts
+// of both in their order. Above, the prefix goes through the kernel for many rows first; then
+// workgroups that hold a sequence's own keys whole join its rows themselves, or again the merge does.
 #include "m3_attend_rows.h"
 
 namespace m3 {
@@ -29,7 +30,7 @@ __device__ __forceinline__ Run run_of(const AttendDev& a, int e, int h, int rin,
 }
 
 template <typename T>
-__global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int splits_a, int team) {
+__global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int team) {
     __shared__ __align__(16) float o_lds[256 * 4];
     const int D = a.D, width = D <= 128 ? 32 : 64, crews = 256 / width;
     const int crew = threadIdx.x / width, lane = threadIdx.x % width, member = crew % team;
@@ -57,17 +58,16 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int spli
             const Group gr = group_at(a, g);
             const int64_t r = (tok - gr.row0) * a.group + head % a.group;
             if (tok >= gr.row0 && tok - gr.row0 < gr.n && gr.held > 0) {
-                if (splits_a) {
+                if (a.splits_a) {
                     const int64_t every = a.b.tokens * a.q_heads;
-                    pre = Run{cut_of((gr.held + kTile - 1) / kTile, splits_a, kPrefixPiece).pieces, at, at, every};
+                    pre = Run{cut_of((gr.held + kTile - 1) / kTile, a.splits_a, kPrefixPiece).pieces, at, at, every};
                 } else {
                     pre = run_of(a, int(group_pair_at(a, g, r / a.rows)), h, int(r % a.rows), a.solo_a + at);
                 }
             }
         }
         const int r = int(t) * a.group + head % a.group;
-        if (a.items) own = run_of(a, a.items_a + int(pair_at(a, i, r / a.rows)), h, r % a.rows, a.solo_b + at);
-        else own = Run{1, a.solo_b + at, 0, 0};
+        own = run_of(a, a.items_a + int(pair_at(a, i, r / a.rows)), h, r % a.rows, a.solo_b + at);
     }
     const int parts = pre.n + own.n;
     auto place = [&](int p) { return p < pre.n ? pre.at(p) : own.at(p - pre.n); };
@@ -111,10 +111,10 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int spli
 
 hipError_t launch_rows_parts(const AttendDev& d, m3_dtype io, hipStream_t s) { return launch_rows_form<kParts>(d, io, s); }
 
-hipError_t launch_merge(const AttendDev& d, int splits_a, m3_dtype io, hipStream_t s) {
+hipError_t launch_merge(const AttendDev& d, m3_dtype io, hipStream_t s) {
     const JoinGrid g = join_grid(d);
-    if (io == M3_BF16) hipLaunchKernelGGL((attend_merge_kernel<bf16_t>), g.grid, dim3(256), 0, s, d, splits_a, g.team);
-    else hipLaunchKernelGGL((attend_merge_kernel<float>), g.grid, dim3(256), 0, s, d, splits_a, g.team);
+    if (io == M3_BF16) hipLaunchKernelGGL((attend_merge_kernel<bf16_t>), g.grid, dim3(256), 0, s, d, g.team);
+    else hipLaunchKernelGGL((attend_merge_kernel<float>), g.grid, dim3(256), 0, s, d, g.team);
     return hipGetLastError();
 }
 
