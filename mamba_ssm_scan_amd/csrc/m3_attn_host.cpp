@@ -234,10 +234,12 @@ static AttendPlan one_pass_plan(const m3_kv_cache& c, const m3_kv_batch& b, cons
 // sequence. 16 rows a tile in either case (32 leave registers for one wave a SIMD: 16 steps
 // behind 8192 tokens 27 us and 33).
 //   The groups' row tiles are items of the launch for few rows, whose waves each convert the
-// keys anew, up to 8192 (row tile, key head, tile of 64 keys) triples; beyond, the kernel for many rows
-// converts them once for 128 rows (256 where these alone fill a quarter of the chip, and parts are few)
-// in a launch of its own. Steps with 16 heads over 4 of 128: behind 8192 tokens 16 / 32 / 64 sequences 27 / 34
-// / 49 us and 32 / 38 / 46, behind 65536 4 / 8 / 16 of them 36 / 47 / 72 and 48 / 49 / 51.
+// keys anew, up to 8192 (row tile, key head, tile of 64 keys) triples, and while the sequences' own
+// row tiles do not fill the chip by themselves; beyond, the kernel for many rows
+// converts them once for 128 rows (256 where these alone fill a quarter of the chip, and parts
+// are few) in a launch of its own. Steps with 16 heads over 4 of 128: behind 8192 tokens 16 / 32 / 64
+// sequences 27 / 34 / 49 us and 32 / 38 / 46, behind 65536 4 / 8 / 16 of them 36 / 47 / 72 and 48 / 49 / 51;
+// 128 of them behind 4096 54 and 40.
 static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view,
                              int32_t q_heads, m3_dtype io) {
     PrefixPlan f{};
@@ -258,7 +260,7 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
     p.packed = b.cu_q && 2 * packed <= b.batch * p.row_tiles;
     const int64_t own = p.packed ? packed : b.batch * p.row_tiles;
     const int64_t full = width == 2 ? 256 : 512, shared = count(16);  // workgroups at once
-    f.tile = std::min(shared, busy(16)) * c.heads * pre > 8192 || shared + own > kAttendItems ||
+    f.tile = std::min(shared, busy(16)) * c.heads * pre > 8192 || own * c.heads >= full || shared + own > kAttendItems ||
              (shared + own) * (tiles + 4) > INT32_MAX;
     size_t rows = 0;  // of parts
     if (!f.tile) {
@@ -293,16 +295,20 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
     return p;
 }
 
-// Parts where they save enough: without them every sequence reads its group's prefix (from L2 or
-// the last cache level, mostly), for rows that the products hardly notice; with them there are
-// the parts to write and a launch to join them.
-constexpr int64_t kPartsBytes = int64_t(4) << 20;
+// Parts where they save enough. Without them every sequence takes its group's prefix tile by
+// tile (from L2 or the last cache level, mostly) for its few rows; with them 16 rows do, but there
+// are parts to write and join. From prefixes of 32 tiles (2048 tokens) on, where at least
+// 1024 passes of a row tile over a tile of 64 keys at headdim 128 are saved: 16 heads over 4 of 128, parts and one
+// pass, behind 2048 tokens 8 / 16 / 64 sequences 17 / 18 / 29 us and 16 / 23 / 37, behind 8192 2 / 4 / 16 / 128
+// of them 18 / 18 / 27 / 47 and 17 / 23 / 37 / 129, behind 512 tokens 16 / 64 of them 17 / 24 and 15 / 17.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
                        m3_dtype io) {
     const AttendPlan p = one_pass_plan(c, b, view, q_heads, io);
     if (view.groups == 0 || view.window > 0 || p.tile || b.batch <= view.groups) return p;
-    const int64_t prefix = std::min(b.max_kv, view.max_prefix * c.page_size) * 2 * c.heads * c.headdim;
-    return (b.batch - view.groups) * double(prefix) < double(kPartsBytes) ? p : parts_plan(p, c, b, view, q_heads, io);
+    const int64_t group = q_heads / c.heads, pre = (std::min(b.max_kv, view.max_prefix * c.page_size) + 63) / 64;
+    const int64_t apart = b.tokens * group / p.rows + b.batch, together = b.tokens * group / 16 + view.groups;
+    const int64_t alone = std::min(b.batch * p.row_tiles, apart), dim = c.headdim <= 64 ? 64 : c.headdim <= 128 ? 128 : 256;
+    return pre >= 32 && (alone - together) * double(c.heads * pre * dim) >= 1024. * 128 ? parts_plan(p, c, b, view, q_heads, io) : p;
 }
 
 }  // namespace m3
