@@ -384,19 +384,27 @@ class KVCache:
             out = q.new_empty(shape)
         o = _dense(out, "out", dev, dt, shape)
         z = q.new_empty((T, H), dtype=torch.float32) if lse else None
-        shared = (0, 0, None, None, None)
-        if prefix is not None:
-            if prefix.device != dev:
-                raise ValueError(f"prefix must be on {dev}")
-            shared = prefix._c
-        view = M3KvView(1 if causal else 0, window, sinks, *shared)
-        key = (b.batch, T, b.max_pages, b.max_q, b.max_kv, cu_q is None, H, code, view.causal, window, sinks, *shared[:2])
+        causal = 1 if causal else 0
+        key = (b.batch, T, b.max_pages, b.max_q, b.max_kv, cu_q is None, H, code, causal, window)
+        view = None
+        if prefix is not None or sinks:
+            shared = (0, 0, None, None, None)
+            if prefix is not None:
+                if prefix.device != dev:
+                    raise ValueError(f"prefix must be on {dev}")
+                shared = prefix._c
+            view = M3KvView(causal, window, sinks, *shared)
+            key = (*key, sinks, shared[0], shared[1], shared[2] is None)
         n = self._sizes.get(key)
         if n is None:
             if len(self._sizes) > 4096:
                 self._sizes.clear()
-            n = self._sizes[key] = lib.m3_kv_attend_view_workspace_size(self._c, b, view, H, code)
+            n = self._sizes[key] = (lib.m3_kv_attend_workspace_size(self._c, b, H, code, causal, window) if view is None else
+                                    lib.m3_kv_attend_view_workspace_size(self._c, b, view, H, code))
         ws = q.new_empty(n, dtype=torch.uint8) if n else None
-        check(lib.m3_kv_attend_view(self._c, b, view, rq, o, z.data_ptr() if lse else None, H, code, scale,
-                                    ws.data_ptr() if n else None, n, _handle(dev)))
+        zp, wp = z.data_ptr() if lse else None, ws.data_ptr() if n else None
+        if view is None:
+            check(lib.m3_kv_attend(self._c, b, rq, o, zp, H, code, scale, causal, window, wp, n, _handle(dev)))
+        else:
+            check(lib.m3_kv_attend_view(self._c, b, view, rq, o, zp, H, code, scale, wp, n, _handle(dev)))
         return (out, z) if lse else out

@@ -21,16 +21,28 @@ __device__ __forceinline__ int own_key(const AttendDev& a, int64_t i) { return p
 // first tile but not its last writes part 0 to its slot 2 w + 1, a later share w
 // the next part to slot 2 w. Every workgroup forms the items' first tiles itself
 // (one scan of the lengths), the first also stores them for the join. Returns the
-// tiles of a share: a multiple of 4, one tile a wave at least. (kView, kParts: an item counts
-// a multiple of 4 tiles, the last ones empty, so that shares of 4 hold one run each: two runs
-// one after the other are twice the latency where there are few. 18 tiles of each of 4
-// heads: 15 us and FIGURE_PAD.)
+// tiles of a share: a multiple of 4, one tile a wave at least.
+//   In the forms other than kPlain runs count a multiple of the share, their last tiles empty, so that
+// a share holds one run: two short ones, one after the other, are twice the latency (about 8 us,
+// where a tile more a wave is 3). There are heads * (items with keys) runs; shares of S tiles
+// are enough where heads * (all / S + items with keys) <= workgroups. Where that would take 8 tiles
+// more than even ones, runs count a multiple of 4 only. 18 tiles of each of 4 heads: 15 us and 10.7; FIGURE_RUNS.
+// Sums over the lanes up to each one: moves within rows of 16, then from rows before (no LDS).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // from 1, 2, 4, 8 lanes before
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of the row before, for rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31, for rows 2 and 3
+    return v;
+}
 template <Form F>
 __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* scan) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int per = (a.items + 64 * kWaves - 1) / (64 * kWaves);
     const int e0 = threadIdx.x * per, e1 = min(e0 + per, a.items);
-    int sum = 0;
+    int sum = 0, held = 0;
     for (int e = e0; e < e1; ++e) {
         int n = 0;
         if (F == kParts && e < a.items_a) {
@@ -49,13 +61,40 @@ __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* 
         if (F != kPlain) n = (n + 3) / 4 * 4;
         first[e] = n;
         sum += n;
+        held += n > 0;
     }
-    int up = sum;  // over the wave, then over the waves before
+    int unit = 0;  // tiles that runs count a multiple of
+    if constexpr (F != kPlain) {
+        const int all = wave_scan(sum), runs = wave_scan(held) * a.c.heads;
+        if (lane == 63) {
+            scan[wave] = all;
+            scan[kWaves + wave] = runs;
+        }
+        __syncthreads();
+        int64_t total = 0, n = 0;
 #pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const int o = __shfl_up(up, k);
-        up += lane >= k ? o : 0;
+        for (int w = 0; w < kWaves; ++w) {
+            total += scan[w];
+            n += scan[kWaves + w];
+        }
+        total *= a.c.heads;
+        const int64_t even = (total + 4 * a.blocks - 1) / (4 * a.blocks) * 4;
+        if (even <= 4) {
+            unit = 4;
+        } else if (n < a.blocks) {
+            const int64_t one = (total + 4 * (a.blocks - n) - 1) / (4 * (a.blocks - n)) * 4;
+            if (one <= even + 8) unit = int(one);
+        }
+        if (unit > 4) {
+            sum = 0;
+            for (int e = e0; e < e1; ++e) {
+                first[e] = (first[e] + unit - 1) / unit * unit;
+                sum += first[e];
+            }
+        }
+        __syncthreads();
     }
+    const int up = wave_scan(sum);  // over the wave, then over the waves before
     if (lane == 63) scan[wave] = up;
     __syncthreads();
     int at = up - sum, total = 0;
@@ -72,7 +111,7 @@ __device__ __forceinline__ int even_shares(const AttendDev& a, int* first, int* 
     if (threadIdx.x == 0) first[a.items] = total;
     __syncthreads();
     const int64_t all = int64_t(total) * a.c.heads;
-    const int share = int((all + 4 * a.blocks - 1) / (4 * a.blocks)) * 4;
+    const int share = unit ? unit : int((all + 4 * a.blocks - 1) / (4 * a.blocks)) * 4;
     if (blockIdx.x == 0) {
         if (threadIdx.x == 0) a.shares[0] = max(share, 4);
         for (int e = threadIdx.x; e <= a.items; e += 64 * kWaves) a.shares[1 + e] = first[e];
@@ -123,7 +162,7 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, FULL, EVEN, F>)
     const int lr = lane & 15, g = lane >> 4;
     const int H = a.c.heads;
     __shared__ int first_lds[EVEN ? kMaxItems + 1 : 1];
-    __shared__ int scan_lds[kWaves];
+    __shared__ int scan_lds[2 * kWaves];
     const int w = int(block_id());
     if (w >= a.blocks) return;
     int64_t x = 0, xe = 1;  // what is left of this workgroup's share
@@ -206,12 +245,18 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, FULL, EVEN, F>)
         const int win_block = F == kView && a.window ? int(max(base + r0 / a.group - a.window + 1, int64_t(0)) / 16) : 0;
         const Prefix pre = F == kView ? prefix_of(a, i) : Prefix{nullptr, 0};
         const int32_t* pages = F == kParts && shared ? gr.pre.pages : a.b.pages + i * a.b.max_pages;
+        // (kParts) the table's end: its entries are read before it is known how many count
+        const int last = int(F != kParts ? 0 : shared ? a.view.max_prefix : a.b.max_pages) - 1;
         auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
             const int pg = blk >> a.shift;
+            if constexpr (F == kParts) {
+                const int p = pages[min(pg, last)];
+                if (blk >= held_blocks || blk < own / 16 || p < 0 || p >= a.c.num_pages) return -1;
+                return ((p * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));
+            }
             // (forms other than kPlain: max_kv ends in the table)
             if (blk >= held_blocks || (F == kPlain && pg >= a.b.max_pages)) return -1;
             if (F == kView && blk < win_block && blk >= sink_blocks) return -1;
-            if (F == kParts && blk < own / 16) return -1;
             const int64_t p = F == kView && pg < pre.count ? pre.pages[pg] : pages[pg];
             if (p < 0 || p >= a.c.num_pages) return -1;
             return ((int(p) * H + h) << a.shift) + (blk & ((1 << a.shift) - 1));

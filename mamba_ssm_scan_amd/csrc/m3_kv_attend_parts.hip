@@ -57,10 +57,10 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int team
         if (g >= 0) {
             const Group gr = group_at(a, g);
             const int64_t r = (tok - gr.row0) * a.group + head % a.group;
-            if (tok >= gr.row0 && tok - gr.row0 < gr.n && gr.held > 0) {
+            if (tok >= gr.row0 && tok - gr.row0 < gr.n) {
                 if (a.splits_a) {
-                    const int64_t every = a.b.tokens * a.q_heads;
-                    pre = Run{cut_of((gr.held + kTile - 1) / kTile, a.splits_a, kPrefixPiece).pieces, at, at, every};
+                    const int n = (gr.held + kTile - 1) / kTile;
+                    pre = Run{n ? cut_of(n, a.splits_a, kPrefixPiece).pieces : 0, at, at, a.b.tokens * a.q_heads};
                 } else {
                     pre = run_of(a, int(group_pair_at(a, g, r / a.rows)), h, int(r % a.rows), a.solo_a + at);
                 }
@@ -71,22 +71,41 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendDev a, int team
     }
     const int parts = pre.n + own.n;
     auto place = [&](int p) { return p < pre.n ? pre.at(p) : own.at(p - pre.n); };
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += width) m = fmaxf(m, a.part_ml[2 * place(p)]);
+    // the first two parts of this crew are on their way while the units' maximum is found
+    const float* po = a.part_o + 4 * lane;
+    const bool mine = 4 * lane < D;
+    floatx4 early[2];
+    float unit[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int p = member + k * team;
+        early[k] = floatx4{0, 0, 0, 0};
+        unit[k] = -INFINITY;
+        if (p < parts) {
+            unit[k] = a.part_ml[2 * place(p)];
+            if (mine) early[k] = *reinterpret_cast<const floatx4*>(po + place(p) * D);
+        }
+    }
+    float2 own_ml{-INFINITY, 0.f};
+    if (lane < parts) own_ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * place(lane));
+    float m = own_ml.x;
+    for (int p = lane + width; p < parts; p += width) m = fmaxf(m, a.part_ml[2 * place(p)]);
     for (int x = 1; x < width; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    float l = 0.f;
-    for (int p = lane; p < parts; p += width) {
+    float l = own_ml.x == -INFINITY ? own_ml.y : own_ml.y * __builtin_amdgcn_exp2f(own_ml.x - m);
+    for (int p = lane + width; p < parts; p += width) {
         const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * place(p));
         l += ml.x == -INFINITY ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - m);
     }
     for (int x = 1; x < width; x <<= 1) l += __shfl_xor(l, x);
     floatx4 v{0, 0, 0, 0};
-    if (4 * lane < D) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v += early[k] * (unit[k] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(unit[k] - m));
+    if (mine) {
 #pragma unroll 4
-        for (int p = member; p < parts; p += team) {
+        for (int p = member + 2 * team; p < parts; p += team) {
             const float mp = a.part_ml[2 * place(p)];
             const float f = mp == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mp - m);
-            v += *reinterpret_cast<const floatx4*>(a.part_o + place(p) * D + 4 * lane) * f;
+            v += *reinterpret_cast<const floatx4*>(po + place(p) * D) * f;
         }
     }
     if (team > 1) {

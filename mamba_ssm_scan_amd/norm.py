@@ -17,7 +17,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .attention import _dense, _device_of, _handle, _on_stream
+from .attention import _complain, _dense, _device_of, _handle, _on_stream
 from .binding import check
 
 GATES = {"identity": 0, "silu": 1, "sigmoid": 2}
@@ -59,17 +59,15 @@ def _lines(t, name: str, device, dtype, shape) -> Optional[M3Lines]:
     """Rows [..., width] where they lie: the entries of a row contiguous, the rows at one stride."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dim() == 2 or not t.numel():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape:
+        _complain(t, name, device, dtype, shape)
+    if t.is_contiguous():
+        return M3Lines(t.data_ptr(), shape[-1])
+    if t.dim() == 2:
         st = t.stride()
-        if t.numel() and st[-1] != 1 and shape[-1] > 1:
+        if st[1] != 1 and shape[1] > 1:
             raise ValueError(f"{name}: the entries of a row must be contiguous")
-        return M3Lines(t.data_ptr(), st[0] if t.dim() == 2 else shape[-1])
+        return M3Lines(t.data_ptr(), st[0])
     try:
         rows = t.detach().view(-1, shape[-1])
     except RuntimeError:
@@ -77,23 +75,28 @@ def _lines(t, name: str, device, dtype, shape) -> Optional[M3Lines]:
     return _lines(rows, name, device, dtype, rows.shape)
 
 
-def _joint(x_dtype, o_dtype, shape, device, gate_fn, scale, post_weight, weight, eps) -> M3Joint:
+def _empty(like: torch.Tensor, dtype) -> torch.Tensor:
+    """A dense tensor of this shape (torch's quickest call for it)."""
+    return torch.empty_like(like) if like.dtype is dtype and like.is_contiguous() else like.new_empty(like.shape, dtype=dtype)
+
+
+def _joint(x_dtype, o_dtype, x, device, gate_fn, scale, post_weight, weight, eps) -> M3Joint:
+    shape = x.shape
     if not shape:
         raise ValueError("rows must be [..., width]")
     W = shape[-1]
-    T = 1
-    for n in shape[:-1]:
-        T *= n
-    if gate_fn not in GATES:
+    fn = GATES.get(gate_fn)
+    if fn is None:
         raise ValueError(f"unknown gate_fn {gate_fn!r}: {', '.join(GATES)}")
-    factor, vec = 1.0, None
+    factor, vec, each = 1.0, None, (W,)
     if isinstance(scale, torch.Tensor):
-        vec = _dense(scale, "scale", device, torch.float32, (W,))
+        vec = _dense(scale, "scale", device, torch.float32, each)
     elif scale is not None:
         factor = float(scale)
-    pw = None if post_weight is None else _dense(post_weight, "post_weight", device, torch.float32, (W,))
-    w = None if weight is None else _dense(weight, "weight", device, torch.float32, (W,))
-    return M3Joint(T, W, binding._io_code(x_dtype), binding._io_code(o_dtype), GATES[gate_fn], eps, factor, vec, pw, w)
+    pw = None if post_weight is None else _dense(post_weight, "post_weight", device, torch.float32, each)
+    w = None if weight is None else _dense(weight, "weight", device, torch.float32, each)
+    return M3Joint(x.numel() // W if W else 0, W, binding._io_code(x_dtype), binding._io_code(o_dtype), fn, eps, factor, vec,
+                   pw, w)
 
 
 class _ResidualNorm(torch.autograd.Function):
@@ -135,24 +138,28 @@ def _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype):
     dev = _device_of(x, "x")
     if o is None and (gate is not None or out is not None):
         raise ValueError("gate or out without o")
-    if out is None and torch.is_grad_enabled() and any(
-            isinstance(t, torch.Tensor) and t.requires_grad for t in (x, o, gate, scale, post_weight, weight)):
-        return _ResidualNorm.apply(x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype)
+    if out is None and torch.is_grad_enabled():
+        for t in (x, o, gate, scale, post_weight, weight):
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                return _ResidualNorm.apply(x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype)
     shape, xt = x.shape, x.dtype
     ot = getattr(o, "dtype", None) if o is not None else xt if dtype is None else dtype
     if dtype is not None and dtype is not ot:
         raise ValueError(f"dtype {dtype} beside an o of {ot}")
-    j = _joint(xt, ot, shape, dev, gate_fn, scale, post_weight, weight, eps)
+    j = _joint(xt, ot, x, dev, gate_fn, scale, post_weight, weight, eps)
     rx = _lines(x, "x", dev, xt, shape)
-    ro = rg = rh = ry = None
-    h = y = None
+    ro = rg = rh = ry = h = y = None
     if o is not None:
-        ro, rg = _lines(o, "o", dev, ot, shape), _lines(gate, "gate", dev, ot, shape)
-        h = x.new_empty(shape) if out is None else out
-        rh = _lines(h, "out", dev, xt, shape)
+        ro = _lines(o, "o", dev, ot, shape)
+        rg = _lines(gate, "gate", dev, ot, shape)
+        if out is None:
+            h = _empty(x, xt)
+            rh = M3Lines(h.data_ptr(), shape[-1])
+        else:
+            h, rh = out, _lines(out, "out", dev, xt, shape)
     if weight is not None:
-        y = x.new_empty(shape, dtype=ot)
-        ry = _lines(y, "y", dev, ot, shape)
+        y = _empty(x, ot)
+        ry = M3Lines(y.data_ptr(), shape[-1])
     check(_lib().m3_residual_norm(j, rx, ro, rg, rh, ry, _handle(dev)))
     return y if o is None else h if weight is None else (h, y)
 
@@ -177,7 +184,7 @@ def _backward(first, dh, dy, h, o, gate, gate_fn, scale, post_weight, weight, ep
     dev, shape = first.device, first.shape
     xt = h.dtype if h is not None else dh.dtype
     ot = o.dtype if o is not None else dy.dtype
-    j = _joint(xt, ot, shape, dev, gate_fn, scale, post_weight, weight, eps)
+    j = _joint(xt, ot, first, dev, gate_fn, scale, post_weight, weight, eps)
     given = {"x": True, "o": o is not None, "gate": gate is not None, "scale": o is not None and j.scale,
              "post_weight": o is not None and j.post_weight, "weight": j.weight}
     ins = [_lines(t, n, dev, d, shape) for t, n, d in ((dh, "dh", xt), (dy, "dy", ot), (h, "h", xt), (o, "o", ot),
@@ -187,7 +194,7 @@ def _backward(first, dh, dy, h, o, gate, gate_fn, scale, post_weight, weight, ep
         if k not in given:
             raise ValueError(f"no gradient {k!r}: {', '.join(_GRADS)}")
         if given[k]:
-            g[k] = (first.new_empty(shape, dtype=xt if k == "x" else ot) if k in ("x", "o", "gate") else
+            g[k] = (_empty(first, xt if k == "x" else ot) if k in ("x", "o", "gate") else
                     first.new_empty(shape[-1], dtype=torch.float32))
     if all(t is None for t in g.values()):
         return g
