@@ -230,8 +230,8 @@ class SharedPrefix:
     pages [groups][max_prefix] int32 names each group's pages, count [groups] int32 how many of them (whole, full pages)
     its sequences share; cu_seqs [groups + 1] int32 the groups' sequences, cu_seqs[g] .. cu_seqs[g + 1] - 1 (None: one
     group of the whole batch). The sequences' positions, lengths and own page tables count the prefix as ever; their
-    own entries for its pages are not read. A sequence outside every group shares nothing. The tensors may change
-    between calls, their sizes not.
+    own entries for its pages are not read. A sequence outside every group shares nothing. The tensors' contents may
+    change between calls; other tensors are another SharedPrefix.
     """
 
     def __init__(self, pages, count, cu_seqs=None):
@@ -245,8 +245,12 @@ class SharedPrefix:
             _dense(cu_seqs, "cu_seqs", dev, torch.int32, (g + 1,))
         elif g != 1:
             raise ValueError(f"{g} groups need cu_seqs")
-        self.pages, self.count, self.cu_seqs, self.device = pages, count, cu_seqs, dev
+        self._pages, self._count, self._cu_seqs, self.device = pages, count, cu_seqs, dev
         self._c = (g, pages.shape[1], cu_seqs.data_ptr() if cu_seqs is not None else None, count.data_ptr(), pages.data_ptr())
+
+    pages = property(lambda self: self._pages)
+    count = property(lambda self: self._count)
+    cu_seqs = property(lambda self: self._cu_seqs)
 
 
 class KVCache:

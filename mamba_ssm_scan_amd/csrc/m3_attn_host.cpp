@@ -218,7 +218,7 @@ static AttendPlan one_pass_plan(const m3_kv_cache& c, const m3_kv_batch& b, cons
         p.blocks = base * p.splits;
         if (p.splits > 1) parts = size_t(p.splits) * size_t(b.tokens) * size_t(q_heads);
     } else if (const int64_t full = width == 2 ? 256 : 512;
-               tiles > 16 && base < full && items <= kAttendItems && items * (tiles + 3) <= INT32_MAX) {
+               tiles > 16 && base < full && items <= kAttendItems && items * (has_view(view) ? 2 * tiles + 16 : tiles) <= INT32_MAX) {
         p.items = int32_t(items);
         // (a share of 4 tiles each; under sinks or prefixes items are multiples of 4)
         p.blocks = std::min<int64_t>(full, has_view(view) ? base * ((tiles + 3) / 4) : (base * tiles + 3) / 4);
@@ -261,7 +261,7 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
     const int64_t own = p.packed ? packed : b.batch * p.row_tiles;
     const int64_t full = width == 2 ? 256 : 512, shared = count(16);  // workgroups at once
     f.tile = std::min(shared, busy(16)) * c.heads * pre > 8192 || own * c.heads >= full || shared + own > kAttendItems ||
-             (shared + own) * (tiles + 4) > INT32_MAX;
+             (shared + own) * (2 * tiles + 16) > INT32_MAX;  // (runs count a multiple of a share)
     size_t rows = 0;  // of parts
     if (!f.tile) {
         f.items = int32_t(shared);
@@ -278,7 +278,7 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
         f.splits = int32_t(std::max<int64_t>(1, (pre + f.split_tiles - 1) / f.split_tiles));
         f.blocks = items * c.heads * f.splits;
         rows = size_t(f.splits) * size_t(every);
-        p.items = tiles > 16 && own * c.heads < full && own <= kAttendItems && own * (tiles + 4) <= INT32_MAX ? int32_t(own) : 0;
+        p.items = tiles > 16 && own * c.heads < full && own <= kAttendItems && own * (2 * tiles + 16) <= INT32_MAX ? int32_t(own) : 0;
         p.blocks = p.items ? std::min<int64_t>(full, own * c.heads * ((tiles + 3) / 4)) : std::max<int64_t>(1, own * c.heads);
     }
     f.slots = rows;

@@ -121,7 +121,8 @@ class _ResidualNorm(torch.autograd.Function):
         dy = grads[-1] if weight is not None else None
         if dh is None and dy is None:
             return (None,) * 9
-        rows = lambda t: None if t is None else t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()  # noqa: E731
+        # (a sum's gradient has no strides, a broadcast one's rows not one stride)
+        rows = lambda t: t if t is None or (t.dim() == 2 and t.stride(1) == 1) else t.contiguous()  # noqa: E731
         need = ctx.needs_input_grad
         g = residual_norm_backward(rows(dh), rows(dy), h if dy is not None else None, o, gate=gate, gate_fn=gate_fn,
                                    scale=factor if scale is None else scale, post_weight=post_weight,

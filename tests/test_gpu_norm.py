@@ -328,6 +328,21 @@ def test_gradients_through_a_stack():
             assert (a.cpu().double() - b).abs().max() <= 1000 * ref.U * b.abs().max()
 
 
+def test_gradients_of_broadcast_results():
+    """Sums over tokens or batches of three-axis rows: gradients whose rows lie at no one stride."""
+    g = gen(16)
+    x, o, w = (torch.randn(s, generator=g).to(DEV).requires_grad_() for s in ((3, 5, 64), (3, 5, 64), (64,)))
+    v = torch.randn(3, 64, generator=g).to(DEV)
+    h, y = norm.residual_norm(x, o, weight=w)
+    got = torch.autograd.grad((y.sum(1) * v).sum() + (h.mean((0, 2)) ** 2).sum(), [x, o, w])
+    a, b, c = (t.detach().cpu().double().requires_grad_() for t in (x, o, w))
+    hh = a + b
+    yy = ref.norm(hh, c, 1e-6)[0]
+    want = torch.autograd.grad((yy.sum(1) * v.cpu().double()).sum() + (hh.mean((0, 2)) ** 2).sum(), [a, b, c])
+    for s, t in zip(got, want):   # rows of 64 terms and sums of 15 rows in fp32: some hundreds of roundings
+        assert (s.cpu().double() - t).abs().max() <= 500 * ref.U * t.abs().max()
+
+
 def test_outside_autograd_and_not_twice():
     p = problem(5, 128, "f32", seed=13)
     leaf = {k: v.requires_grad_() for k, v in dev(p, "x", "o", *NAMES).items()}
