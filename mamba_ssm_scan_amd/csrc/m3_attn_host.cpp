@@ -295,20 +295,27 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
     return p;
 }
 
-// Parts where they save enough. Without them every sequence takes its group's prefix tile by
-// tile (from L2 or the last cache level, mostly) for its few rows; with them 16 rows do, but there
-// are parts to write and join. From prefixes of 32 tiles (2048 tokens) on, where at least
-// 1024 passes of a row tile over a tile of 64 keys at headdim 128 are saved: 16 heads over 4 of 128, parts and one
-// pass, behind 2048 tokens 8 / 16 / 64 sequences 17 / 18 / 29 us and 16 / 23 / 37, behind 8192 2 / 4 / 16 / 128
-// of them 18 / 18 / 27 / 47 and 17 / 23 / 37 / 129, behind 512 tokens 16 / 64 of them 17 / 24 and 15 / 17.
+// Parts where they save enough, by what the prefix takes either way (us; from measurements). A wave's pass of up to 16 rows
+// over a tile of 64 keys at headdim 128 takes 1 / 358 of the chip (32 rows: 1.4 times that), a pass of 128 rows in the
+// kernel for many rows 1 / 136 (256 rows: 1.6 times); passes of fp32 rows half as much again. Parts of
+// their own cost 3 more where the one pass deals out shares and joins anyway, else 10, the launch for many rows 10 to
+// 12 on top. 16 heads over 4 of 128, parts and one pass, behind 512 tokens 16 / 64 sequences 17 / 24 us and 15 / 17;
+// behind 2048 8 / 16 / 64 / 128 of them 17 / 18 / 29 / 35 and 16 / 23 / 37 / 44; behind 8192 2 / 4 / 16 / 128 of them 18
+// / 18 / 24 / 47 and 17 / 23 / 37 / 129.
 AttendPlan attend_plan(const m3_kv_cache& c, const m3_kv_batch& b, const m3_kv_view& view, int32_t q_heads,
                        m3_dtype io) {
-    const AttendPlan p = one_pass_plan(c, b, view, q_heads, io);
-    if (view.groups == 0 || view.window > 0 || p.tile || b.batch <= view.groups) return p;
+    const AttendPlan one = one_pass_plan(c, b, view, q_heads, io);
+    if (view.groups == 0 || view.window > 0 || one.tile || b.batch <= view.groups) return one;
+    const AttendPlan two = parts_plan(one, c, b, view, q_heads, io);
     const int64_t group = q_heads / c.heads, pre = (std::min(b.max_kv, view.max_prefix * c.page_size) + 63) / 64;
-    const int64_t apart = b.tokens * group / p.rows + b.batch, together = b.tokens * group / 16 + view.groups;
-    const int64_t alone = std::min(b.batch * p.row_tiles, apart), dim = c.headdim <= 64 ? 64 : c.headdim <= 128 ? 128 : 256;
-    return pre >= 32 && (alone - together) * double(c.heads * pre * dim) >= 1024. * 128 ? parts_plan(p, c, b, view, q_heads, io) : p;
+    const double scale = double(c.heads * pre) * (c.headdim <= 64 ? 0.5 : c.headdim <= 128 ? 1. : 2.) * (io == M3_F32 ? 1.5 : 1.);
+    auto tiles_of = [&](const int64_t all, int64_t each, int64_t n) { return double(std::min(n * each, b.tokens * group / all + n)); };
+    const double apart = tiles_of(one.rows, one.row_tiles, b.batch) * (one.rows == 32 ? 1.4 : 1.) * scale / 358;
+    const PrefixPlan& f = two.prefix;
+    const double rows = tiles_of(f.rows, f.row_tiles, view.groups) * scale;
+    const double together = f.tile ? rows * f.rows / 128. * (f.rows > 128 ? 0.8 : 1.) / 136 + (one.items ? 15 : 20)
+                                   : rows / 358 + (one.items ? 3 : 10);
+    return together < apart ? two : one;
 }
 
 }  // namespace m3
