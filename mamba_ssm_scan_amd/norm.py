@@ -162,6 +162,8 @@ def _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype):
         y = _empty(x, ot)
         ry = M3Lines(y.data_ptr(), shape[-1])
     check(_lib().m3_residual_norm(j, rx, ro, rg, rh, ry, _handle(dev)))
+    if out is not None:  # what autograd kept of it before is no longer there
+        torch.autograd.graph.increment_version(out)
     return y if o is None else h if weight is None else (h, y)
 
 
@@ -174,8 +176,9 @@ def residual_norm(x, o=None, *, gate=None, gate_fn: str = "silu", scale=None, po
     parts of a fused projection are used where they lie. gate_fn: "silu", "sigmoid" or "identity". scale: fp32
     [width] or a number. post_weight, weight: fp32 [width]; without post_weight o is not normed. Norms are of the
     root mean square, N(v; w) = v w / sqrt(mean v^2 + eps). width: up to 8192. out: where h goes, may be x itself.
-    dtype: y's type without o (x's unless given; with o it is o's). stream: the current one unless given. The results take part in autograd where an input does, unless out is given
-    (as in torch, a backward pass is captured into a graph only while no eager graph of the same leaves lives).
+    dtype: y's type without o (x's unless given; with o it is o's). stream: the current one unless given. The results
+    take part in autograd where an input does, unless out is given (as in torch, a backward pass is captured into a graph
+    only while no eager graph of the same leaves lives).
     """
     return _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype, stream=stream)
 

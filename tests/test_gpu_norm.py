@@ -428,3 +428,14 @@ def test_refusals():
                      ((x, x, x[:2]), dict(weight=w)), ((x, b.half(), x), dict(weight=w))):
         with pytest.raises((ValueError, TypeError, norm.binding.M3Error)):
             norm.residual_norm_backward(*args, **kw)
+
+
+def test_out_that_autograd_still_needs():
+    """A tensor that autograd kept for a backward pass and that `out` then overwrites is found out."""
+    x = torch.randn(4, 64, generator=gen(31)).to(DEV)
+    s = torch.ones(64, device=DEV, requires_grad=True)
+    y = (x * s).sum()
+    with torch.no_grad():
+        norm.residual_norm(x, torch.ones_like(x), out=x)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
