@@ -26,7 +26,7 @@ __device__ __forceinline__ int own_key(const AttendDev& a, int64_t i) { return p
 // a share holds one run: two short ones, one after the other, are twice the latency (about 8 us,
 // where a tile more a wave is 3). There are heads * (items with keys) runs; shares of S tiles
 // are enough where heads * (all / S + items with keys) <= workgroups. Where that would take 8 tiles
-// more than even ones, runs count a multiple of 4 only. 18 tiles of each of 4 heads: 15 us and 10.7; FIGURE_RUNS.
+// more than even ones, runs count a multiple of 4 only. 18 tiles of each of 4 heads: 15 us and 10.7.
 // Sums over the lanes up to each one: moves within rows of 16, then from rows before (no LDS).
 __device__ __forceinline__ int wave_scan(int v) {
     v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // from 1, 2, 4, 8 lanes before

@@ -188,11 +188,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 :
         }
     };
     // The forms other than kPlain have short runs of keys (a window's, a piece of a prefix), and
-    // a wave's waits weigh more: page numbers and the first loads go out together and before
-    // the rows' own, and (kDeep, where registers allow) each tile's loads a turn earlier. 128
-    // steps behind 8192 tokens: FIGURE_DEEP.
-    constexpr bool kDeep = F != kPlain && QT == 1 && !(DP == 256 && NP == 3);
-    Raw ra, rb;
+    // a wave's first waits weigh more: page numbers and the first loads go out together and
+    // before the rows' own (128 steps behind 8192 tokens 1 us of 62). Each tile's loads a turn
+    // earlier than in kPlain gained nothing more.
+    Raw ra, rb;  // rb: the second tile's K before the loop
     Pages pgv{}, pgk{};
     if constexpr (F != kPlain) {
         if (t0 < t1) {
@@ -313,12 +312,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 :
                 stage_k(rb, 1);
             }
         }
-        if constexpr (kDeep) {  // what turn t0 puts into LDS
-            fetch_v(ra, t0 + 1, pgv);
-            fetch_k(ra, t0 + (kAhead ? 2 : 1), kAhead ? pgk : pgv);
-            pgv = pgk;
-            pgk = find(t0 + 3);
-        }
         if constexpr (kAhead) {
             __syncthreads();
             if (seen(t0)) scores(0, s);
@@ -326,14 +319,12 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 :
         __syncthreads();
     }
     float inv_top = -INFINITY;  // scales of a 1 / vs above it ask for the maxima (all, until every row of the wave has a reference)
-    // `put`: what goes to LDS at the turn's end, `get`: what is requested at its start
-    auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4], const Raw& put, Raw& get) {
-        constexpr int kV = kDeep ? 2 : 1, kK = kV + kAhead;  // turns until they are used (nothing after the last)
-        fetch_v(get, tile + kV, pgv);
-        fetch_k(get, tile + kK, kAhead ? pgk : pgv);
-        if constexpr (kAhead || kDeep) {
+    auto turn_of = [&](int tile, int buf, floatx4 (&s)[QT][4], floatx4 (&sn)[QT][4]) {
+        fetch_v(ra, tile + 1, pgv);  // (nothing after the last)
+        fetch_k(ra, tile + 1 + kAhead, kAhead ? pgk : pgv);
+        if constexpr (kAhead) {
             pgv = pgk;
-            pgk = find(tile + (kDeep ? 4 : 3));
+            pgk = find(tile + 3);
         } else {
             pgv = find(tile + 2);
         }
@@ -421,16 +412,15 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 :
         } else if (kAhead && seen(tile + 1)) {
             scores(buf ^ 1, sn);
         }
-        stage_k(put, kAhead ? buf : buf ^ 1);
-        stage_v(put, tile + 1, buf ^ 1);
+        stage_k(ra, kAhead ? buf : buf ^ 1);
+        stage_v(ra, tile + 1, buf ^ 1);
         __syncthreads();
     };
-    Raw& other = kDeep ? rb : ra;
     for (int tile = t0; tile < t1; tile += 2) {
-        turn_of(tile, 0, s, sn, ra, other);
+        turn_of(tile, 0, s, sn);
         if (tile + 1 < t1) {
-            if constexpr (kAhead) turn_of(tile + 1, 1, sn, s, other, ra);
-            else turn_of(tile + 1, 1, s, sn, other, ra);
+            if constexpr (kAhead) turn_of(tile + 1, 1, sn, s);
+            else turn_of(tile + 1, 1, s, sn);
         }
     }
 
