@@ -4,10 +4,16 @@
 // probabilities' sum and the weighted values of each, o = (sum 2^(m - M) o) / (sum 2^(m - M) l).
 // So a group's prefix is one more run of keys, whose rows are all its sequences' rows: read once
 // for as many of them as a row tile holds, where every sequence would read it for a few rows.
-// Up to 64 rows of a key head a group, the groups' row tiles and the sequences' are items of one
-// launch of the kernel for few rows, dealt out in even shares, and a merge takes a row's parts
-// of both in their order. Above, the prefix goes through the kernel for many rows first; then
-// workgroups that hold a sequence's own keys whole join its rows themselves, or again the merge does.
+// While that is little work, the groups' row tiles and the sequences' are items of one launch of
+// the kernel for few rows, dealt out in even shares, and a merge takes a row's parts of both in
+// their order. Above, the prefix goes through the kernel for many rows first; then workgroups
+// that hold a sequence's own keys whole join its rows themselves, or again the merge does. (The plan's
+// rules stand with it, m3_attn_host.cpp.)
+//
+// 16 heads over 4 of 128: 16 steps behind 8192 tokens (int8) 18 us and the merge's 5.7, where latencies
+// decide: 3.4 us until the shares are known, 10 until a first tile is through, 1.6 a tile. 128 steps
+// behind 8192 tokens, 63 .. 1023 of their own (e4m3): prefix 31 us, own keys and the joining 22, of them
+// 14 the own keys' bytes; each sequence by itself 129. The prefix's parts are in fp32, 17 MB of them here.
 #include "m3_attend_rows.h"
 
 namespace m3 {
