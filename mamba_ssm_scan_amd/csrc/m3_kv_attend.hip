@@ -27,7 +27,7 @@
 // tokens (int8) 70 us, 3.9 TB/s, where 128 of 2112 each reach 5.1: the longest of a
 // workgroup's sequences decides. One sequence of 2048 is a chain of latencies (lengths,
 // page, codes, then the join's launch, as its 32 tiles are split over workgroups of four
-// waves): 8.5 and 4.5 us. 16 sequences of 8000 with 4 rows each (16 heads over 4 of 128): 36
+// waves): 8.5 and 3.9 us. 16 sequences of 8000 with 4 rows each (16 heads over 4 of 128): 36
 // us, of 64 of 2000 in fp32 (8 over 2) 29.
 #include "m3_attend_rows.h"
 
@@ -81,22 +81,42 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
     }
     if (!live) parts = 0;
     auto place = [&](int p) { return p ? p1 + p * step : p0; };
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += width) m = fmaxf(m, a.part_ml[2 * place(p)]);
+    // The first two parts of this crew are on their way while the units' maximum is found (4.5 us
+    // before, 3.9 since: one sequence under a window of 1024).
+    const float* po = a.part_o + 4 * lane;
+    const bool mine = 4 * lane < D;
+    floatx4 early[2];
+    float unit[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int p = member + k * team;
+        early[k] = floatx4{0, 0, 0, 0};
+        unit[k] = -INFINITY;
+        if (p < parts) {
+            unit[k] = a.part_ml[2 * place(p)];
+            if (mine) early[k] = *reinterpret_cast<const floatx4*>(po + place(p) * D);
+        }
+    }
+    float2 own_ml{-INFINITY, 0.f};
+    if (lane < parts) own_ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * place(lane));
+    float m = own_ml.x;
+    for (int p = lane + width; p < parts; p += width) m = fmaxf(m, a.part_ml[2 * place(p)]);
     for (int x = 1; x < width; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
-    float l = 0.f;
-    for (int p = lane; p < parts; p += width) {
+    float l = own_ml.x == -INFINITY ? own_ml.y : own_ml.y * __builtin_amdgcn_exp2f(own_ml.x - m);
+    for (int p = lane + width; p < parts; p += width) {
         const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * place(p));
         l += ml.x == -INFINITY ? ml.y : ml.y * __builtin_amdgcn_exp2f(ml.x - m);
     }
     for (int x = 1; x < width; x <<= 1) l += __shfl_xor(l, x);
     floatx4 v{0, 0, 0, 0};
-    if (4 * lane < D) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v += early[k] * (unit[k] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(unit[k] - m));
+    if (mine) {
 #pragma unroll 4
-        for (int p = member; p < parts; p += team) {
+        for (int p = member + 2 * team; p < parts; p += team) {
             const float mp = a.part_ml[2 * place(p)];
             const float f = mp == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mp - m);
-            v += *reinterpret_cast<const floatx4*>(a.part_o + place(p) * D + 4 * lane) * f;
+            v += *reinterpret_cast<const floatx4*>(po + place(p) * D) * f;
         }
     }
     if (team > 1) {
