@@ -27,7 +27,7 @@
 // tokens (int8) 70 us, 3.9 TB/s, where 128 of 2112 each reach 5.1: the longest of a
 // workgroup's sequences decides. One sequence of 2048 is a chain of latencies (lengths,
 // page, codes, then the join's launch, as its 32 tiles are split over workgroups of four
-// waves): 8.5 and 3.9 us. 16 sequences of 8000 with 4 rows each (16 heads over 4 of 128): 36
+// waves): 8.4 and 4.4 us. 16 sequences of 8000 with 4 rows each (16 heads over 4 of 128): 36
 // us, of 64 of 2000 in fp32 (8 over 2) 29.
 #include "m3_attend_rows.h"
 
@@ -81,8 +81,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendDev a, int team)
     }
     if (!live) parts = 0;
     auto place = [&](int p) { return p ? p1 + p * step : p0; };
-    // The first two parts of this crew are on their way while the units' maximum is found (4.5 us
-    // before, 3.9 since: one sequence under a window of 1024).
+    // The first two parts of this crew are on their way while the units' maximum is found (4.4 us
+    // at the least before, 3.8 since: one sequence under a window of 1024).
     const float* po = a.part_o + 4 * lane;
     const bool mine = 4 * lane < D;
     floatx4 early[2];

@@ -8,7 +8,7 @@
 // conversion, one after the other), the masks of the sinks' tile and of the window's ends, the first tile's
 // maximum, the rows' way out. Workgroups of 4 waves and 128 rows, two a CU, hide that wait but convert
 // each key twice as often: 233 us (window 512: 156 and 159).
-// Eight questions of 256 behind 16384 tokens: 314 us with the join, 876 TFLOP/s.
+// Eight questions of 256 behind 16384 tokens: 313 us with the join, 880 TFLOP/s.
 #include "m3_attend_tile.h"
 
 namespace m3 {

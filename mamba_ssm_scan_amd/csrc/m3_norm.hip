@@ -12,8 +12,8 @@
 // sum over it takes a butterfly in each wave and one exchange through LDS. The vectors stay
 // in registers over a workgroup's rows, and the next row's loads are issued before this
 // row's sums. 8192 rows of 2048, all parts: forward with an fp32 stream 43 us (5.4 TB/s), backward
-// in bf16 53 + 4 us for the joining of its sums (5.0 TB/s); 16384 of 4096, fp32 stream: 179 and
-// 279 + 5 us (5.3 TB/s both); one step of 128 rows 3.5 us, a launch's least. Rows that are not
+// in bf16 53 + 4 us for the joining of its sums (5.0 TB/s); 16384 of 4096, fp32 stream: 174 and
+// 269 + 4 us (5.4 and 5.5 TB/s); one step of 128 rows 3.5 us, a launch's least. Rows that are not
 // 16-byte aligned (1999 of 1283, fp32): 23 + 4 us at 3.5 TB/s, entry by entry; 16-byte loads at any
 // alignment took 31 us, as the hardware splits them.
 #include <algorithm>
