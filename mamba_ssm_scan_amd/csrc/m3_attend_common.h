@@ -36,6 +36,7 @@ struct AttendDev {
     int64_t blocks;  // workgroups with work (the grid may hold a few more)
     Form form;
     m3_kv_view view;
+    int most_prefix;  // pages that a prefix may have: of a row of its table, ending within 32 bits
     // The kParts form: the groups' (group, row tile) pairs come before the sequences' among the
     // items, numbered by their own row tiles; where parts lie (in rows of part_o, part_ml).
     int items_a, packed_a, splits_a;  // splits_a: the prefix's parts by [split][token][head]; 0: even shares too
@@ -102,7 +103,7 @@ struct Prefix {
 __device__ __forceinline__ Prefix prefix_at(const AttendDev& a, int64_t g) {
     const m3_kv_view& v = a.view;
     if (g < 0) return Prefix{nullptr, 0};
-    return Prefix{v.prefix_pages + g * v.max_prefix, min(max(v.prefix_count[g], 0), int(v.max_prefix))};
+    return Prefix{v.prefix_pages + g * v.max_prefix, min(max(v.prefix_count[g], 0), a.most_prefix)};
 }
 __device__ __forceinline__ Prefix prefix_of(const AttendDev& a, int64_t i) { return prefix_at(a, group_of(a, i)); }
 

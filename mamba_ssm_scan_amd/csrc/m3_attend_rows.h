@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * kWaves, (kSimdWaves<T, DP, QT, FULL, EVEN, F>)
         const Prefix pre = F == kView ? prefix_of(a, i) : Prefix{nullptr, 0};
         const int32_t* pages = F == kParts && shared ? gr.pre.pages : a.b.pages + i * a.b.max_pages;
         // (kParts) the table's end: its entries are read before it is known how many count
-        const int last = int(F != kParts ? 0 : shared ? a.view.max_prefix : a.b.max_pages) - 1;
+        const int last = F != kParts ? 0 : int((shared ? a.view.max_prefix : a.b.max_pages) - 1);
         auto find = [&](int blk) {  // a block's index for this head, -1: none (there are fewer than 2^31)
             const int pg = blk >> a.shift;
             if constexpr (F == kParts) {

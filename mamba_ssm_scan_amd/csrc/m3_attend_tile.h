@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 && !(F == kView && QT == 2) ? 3 :
             const int blk = tile_at<F>(sp, tile) * 4 + (64 * swave + NT * j) / DP, pg = blk >> a.shift;
             r.p[j] = -1;
             if constexpr (F == kParts) {  // (read before it is known how many entries count)
-                const int p = pages[min(pg, int(a.view.max_prefix) - 1)];
+                const int p = pages[min(pg, int(a.view.max_prefix - 1))];
                 if (tile < t1 && blk < held_blocks) r.p[j] = p;
                 continue;
             }

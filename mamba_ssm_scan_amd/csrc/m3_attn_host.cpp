@@ -114,14 +114,13 @@ m3_kv_batch bounded(const m3_kv_batch& b, const m3_kv_cache& c) {
 // the plain view of m3_kv_attend
 m3_kv_view plain(int32_t causal, int64_t window) { return m3_kv_view{causal ? 1 : 0, window, 0, 0, 0, nullptr, nullptr, nullptr}; }
 // A view whose window's end no position reaches, so that sums with it stay in range; as for
-// sinks; and prefixes that end within 32 bits.
-m3_kv_view bounded(const m3_kv_view& v, const m3_kv_cache& c) {
+// sinks. (max_prefix is a stride too: its bound is the launch's, most_prefix.)
+m3_kv_view bounded(const m3_kv_view& v) {
     m3_kv_view r = v;
     r.causal = v.causal ? 1 : 0;
     r.window = std::min(v.window, int64_t(1) << 31);
     r.sinks = v.window > 0 ? std::min(v.sinks, (int64_t(1) << 31) - 256) : 0;  // (as max_kv)
-    r.max_prefix = std::min(v.max_prefix, ((int64_t(1) << 31) - 256) / c.page_size);
-    if (r.max_prefix == 0) r.groups = 0;
+    if (v.max_prefix == 0) r.groups = 0;
     return r;
 }
 
@@ -458,7 +457,7 @@ size_t m3_kv_attend_view_workspace_size(const m3_kv_cache* cache, const m3_kv_ba
                                         int32_t q_heads, m3_dtype io_dtype) {
     clear_error();
     if (check_attend(cache, batch, view, q_heads, io_dtype) != M3_OK) return 0;
-    return m3::attend_plan(*cache, bounded(*batch, *cache), bounded(*view, *cache), q_heads, io_dtype).total;
+    return m3::attend_plan(*cache, bounded(*batch, *cache), bounded(*view), q_heads, io_dtype).total;
 }
 
 m3_status m3_kv_attend(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_rows* q, void* out, float* lse,
@@ -481,7 +480,7 @@ m3_status m3_kv_attend_view(const m3_kv_cache* cache, const m3_kv_batch* batch, 
     if (!aligned(out, 16)) return set_error(M3_EALIGN, "out is not 16-byte aligned");
     if (!aligned(lse, 4)) return set_error(M3_EALIGN, "lse is not 4-byte aligned");
     if (!std::isfinite(scale)) return set_error(M3_EINVAL, "scale is not finite");
-    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, bounded(*view, *cache),
+    m3::AttendArgs a{*cache, bounded(*batch, *cache), *q, out, lse, q_heads, io_dtype, scale, bounded(*view),
                      {}, workspace, wide_rows(*q, es), reinterpret_cast<hipStream_t>(stream)};
     a.plan = m3::attend_plan(*cache, a.b, a.view, q_heads, io_dtype);
     const size_t rows = size_t(T) * size_t(q_heads);

@@ -102,7 +102,7 @@ struct AttendArgs {
     int32_t q_heads;
     m3_dtype io;
     float scale;
-    m3_kv_view view;      // sinks 0 without a window, max_prefix bounded
+    m3_kv_view view;      // sinks 0 without a window
     AttendPlan plan;
     void* workspace;
     bool wide;

@@ -184,6 +184,7 @@ hipError_t launch_kv_attend(const AttendArgs& a) {
     d.blocks = p.blocks;
     d.form = p.parts ? kParts : has_view(a.view) ? kView : kPlain;
     d.view = a.view;
+    d.most_prefix = int(std::min(a.view.max_prefix, ((int64_t(1) << 31) - 256) / a.c.page_size));
     hipError_t e;
     if (!p.parts) {
         if (p.tile) {

@@ -128,3 +128,21 @@ def test_the_prefix_of_one_pass():
                                        visible(torch.arange(l - rows, l), l, True, 0, 0))
             keep = ~want[i]
             within(out[i * rows:(i + 1) * rows].cpu()[keep], o[keep], ref.attend_bound(o, mag, top, D, l, BF)[keep], f"out {i}")
+
+
+@pytest.mark.parametrize("wide", [2047, 2048, 4096])
+def test_prefix_tables_wider_than_positions(wide):
+    """Pages of 2^20 tokens: a table may name more than 2^31 tokens' worth; its rows lie where they are."""
+    D, page = 16, 1 << 20
+    c = attention.KVCache.empty(3, page, 1, D, dtype=I8)
+    g = torch.Generator().manual_seed(wide)
+    k, v = torch.randn(150, 1, D, generator=g), torch.randn(150, 1, D, generator=g)
+    own = ints([[0], [1], [-1]])
+    c.append(k.to(DEV), v.to(DEV), ints([60, 90]), own[:2].contiguous(), cu_q=ints([0, 60, 150]), max_q=90)
+    table = torch.full((2, wide), -1, dtype=torch.int32, device=DEV)
+    table[0, 0], table[1, 0] = 0, 1
+    q = torch.randn(3, 2, D, generator=g).to(DEV)
+    lens = ints([60, 90, 80])
+    got = c.attend(q, lens, torch.full_like(own, -1), prefix=attention.SharedPrefix(table, ints([1, 1]), ints([0, 1, 3])))
+    want = c.attend(q, lens, ints([[0], [1], [1]]))
+    assert want.abs().amin(-1).max() > 0 and (got - want).abs().max() <= 2.0 ** -18 * want.abs().max()
