@@ -118,7 +118,7 @@ class HybridStack:
 
         x = self._run(u, layer_of)
         self.kv_len.fill_(L)
-        self.prefix = attention.SharedPrefix(self.pages[:1].contiguous(), torch.tensor([full], dtype=torch.int32, device="cuda"))
+        self.prefix = attention.SharedPrefix(self.pages[:1, :full].contiguous(), torch.tensor([full], dtype=torch.int32, device="cuda"))
         return x
 
     def step(self, u):

@@ -195,7 +195,7 @@ typedef struct m3_kv_view {
     int64_t window;              /* 0: none */
     int64_t sinks;               /* >= 0 */
     int64_t groups;              /* 0: no prefixes */
-    int64_t max_prefix;          /* pages of a row of prefix_pages */
+    int64_t max_prefix;          /* pages of a row of prefix_pages; sizes the launch, as max_kv does */
     const int32_t* group_start;  /* [groups + 1] or NULL */
     const int32_t* prefix_count; /* [groups] */
     const int32_t* prefix_pages; /* [groups][max_prefix] */

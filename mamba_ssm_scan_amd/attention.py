@@ -231,7 +231,8 @@ class SharedPrefix:
     its sequences share; cu_seqs [groups + 1] int32 the groups' sequences, cu_seqs[g] .. cu_seqs[g + 1] - 1 (None: one
     group of the whole batch). The sequences' positions, lengths and own page tables count the prefix as ever; their
     own entries for its pages are not read. A sequence outside every group shares nothing. The tensors' contents may
-    change between calls; other tensors are another SharedPrefix.
+    change between calls; other tensors are another SharedPrefix. A launch is sized by the table's width: one much wider than the
+    prefixes costs time.
     """
 
     def __init__(self, pages, count, cu_seqs=None):
