@@ -12,6 +12,7 @@ and workspaces allocated with torch on the call's stream, no other implementatio
 from __future__ import annotations
 
 import ctypes
+import warnings
 from typing import Optional
 
 import torch
@@ -134,15 +135,34 @@ class _ResidualNorm(torch.autograd.Function):
 _GRADS = ("x", "o", "gate", "scale", "post_weight", "weight")
 
 
+def _no_graph_through(out, x, asked: bool):
+    """Refuses an `out` that autograd would go on taking for what it held before, or whose h would stand for an x that has
+    no o in it; says so where a gradient that is asked for ends at an `out` of its own."""
+    if not isinstance(out, torch.Tensor):
+        return
+    if out.requires_grad or (asked and (out is x or (out.numel() > 0 and out.data_ptr() == x.data_ptr()))):
+        raise RuntimeError("out takes no part in autograd: it may neither require a gradient nor, where an input does, be "
+                           "x itself (torch.no_grad() where none is wanted)")
+    if asked:
+        warnings.warn("residual_norm: the results take no part in autograd, as out is given (torch.no_grad() says that "
+                      "none is wanted)", stacklevel=5)
+
+
 @_on_stream
 def _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype):
     dev = _device_of(x, "x")
     if o is None and (gate is not None or out is not None):
         raise ValueError("gate or out without o")
-    if out is None and torch.is_grad_enabled():
+    if torch.is_grad_enabled():
+        asked = False
         for t in (x, o, gate, scale, post_weight, weight):
             if isinstance(t, torch.Tensor) and t.requires_grad:
-                return _ResidualNorm.apply(x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype)
+                asked = True
+                break
+        if out is not None:
+            _no_graph_through(out, x, asked)
+        elif asked:
+            return _ResidualNorm.apply(x, o, gate, scale, post_weight, weight, gate_fn, eps, dtype)
     shape, xt = x.shape, x.dtype
     ot = getattr(o, "dtype", None) if o is not None else xt if dtype is None else dtype
     if dtype is not None and dtype is not ot:
@@ -177,8 +197,9 @@ def residual_norm(x, o=None, *, gate=None, gate_fn: str = "silu", scale=None, po
     [width] or a number. post_weight, weight: fp32 [width]; without post_weight o is not normed. Norms are of the
     root mean square, N(v; w) = v w / sqrt(mean v^2 + eps). width: up to 8192. out: where h goes, may be x itself.
     dtype: y's type without o (x's unless given; with o it is o's). stream: the current one unless given. The results
-    take part in autograd where an input does, unless out is given (as in torch, a backward pass is captured into a graph
-    only while no eager graph of the same leaves lives).
+    take part in autograd where an input does (as in torch, a backward pass is captured into a graph only while no eager
+    graph of the same leaves lives). With out they take no part, which is said by a warning where an input requires a
+    gradient; an out that requires one, or that is then x itself, is refused (both hold while gradients are recorded).
     """
     return _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype, stream=stream)
 
