@@ -20,6 +20,7 @@ import math
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding
 from .binding import check
@@ -134,6 +135,15 @@ def _on_stream(fn):
         with torch.cuda.stream(stream):
             return fn(first, *args, **kw)
     return call
+
+
+def _no_tangents(name: str, *tensors):
+    """Refuses inputs that carry a tangent of forward-mode differentiation, which the results would lose."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # (none is being formed)
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 # the current stream's raw handle, without the Stream object around it where torch has that call

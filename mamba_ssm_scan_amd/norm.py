@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import binding
-from .attention import _complain, _dense, _device_of, _handle, _on_stream
+from .attention import _complain, _dense, _device_of, _handle, _no_tangents, _on_stream
 from .binding import check
 
 GATES = {"identity": 0, "silu": 1, "sigmoid": 2}
@@ -153,6 +153,7 @@ def _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype):
     dev = _device_of(x, "x")
     if o is None and (gate is not None or out is not None):
         raise ValueError("gate or out without o")
+    _no_tangents("residual_norm", x, o, gate, scale, post_weight, weight)
     if torch.is_grad_enabled():
         asked = False
         for t in (x, o, gate, scale, post_weight, weight):
@@ -199,7 +200,8 @@ def residual_norm(x, o=None, *, gate=None, gate_fn: str = "silu", scale=None, po
     dtype: y's type without o (x's unless given; with o it is o's). stream: the current one unless given. The results
     take part in autograd where an input does (as in torch, a backward pass is captured into a graph only while no eager
     graph of the same leaves lives). With out they take no part, which is said by a warning where an input requires a
-    gradient; an out that requires one, or that is then x itself, is refused (both hold while gradients are recorded).
+    gradient; an out that requires one, or that is then x itself, is refused (both hold while gradients are recorded). Inputs
+    with tangents of forward-mode differentiation are refused.
     """
     return _forward(x, o, gate, gate_fn, scale, post_weight, weight, eps, out, dtype, stream=stream)
 
@@ -246,6 +248,7 @@ def residual_norm_backward(dh, dy, h, o=None, *, gate=None, gate_fn: str = "silu
         raise ValueError("neither dh nor dy is given")
     if dy is not None and h is None:
         raise ValueError("dy without h")
+    _no_tangents("residual_norm_backward", dh, dy, h, o, gate, scale, post_weight, weight)
     first = dh if dh is not None else dy
     _device_of(first, "dh" if dh is not None else "dy")
     return _backward(first, dh, dy, h if dy is not None else None, o, gate, gate_fn, scale, post_weight, weight, eps, want,

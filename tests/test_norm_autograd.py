@@ -86,3 +86,39 @@ def test_nothing_is_said_where_no_gradient_is_asked_for(calls):
         norm.residual_norm(**t, out=t["x"])
         norm.residual_norm(**t, out=torch.empty(T, W))
     assert len(calls) == 5
+
+
+@pytest.mark.parametrize("dual", GIVEN)
+@pytest.mark.parametrize("also", ["", "asked", "no_grad", "out"])
+def test_forward_mode_is_refused(calls, dual, also):
+    """An input with a tangent, which the results would not carry on; also where a gradient is asked for as well."""
+    from torch.autograd import forward_ad
+    t = tensors(*(GIVEN if also == "asked" else ()))
+    with forward_ad.dual_level():
+        t[dual] = forward_ad.make_dual(t[dual], torch.ones_like(t[dual]))
+        with pytest.raises(NotImplementedError, match="forward"), torch.set_grad_enabled(also != "no_grad"):
+            norm.residual_norm(**t, out=torch.empty(T, W) if also == "out" else None)
+        assert not calls
+        norm.residual_norm(**tensors())                      # no tangent: as ever
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("dual", ["dh", "dy", "h", "o", "weight"])
+def test_forward_mode_is_refused_by_the_gradients_too(calls, dual):
+    from torch.autograd import forward_ad
+    t = dict(dh=torch.ones(T, W), dy=torch.ones(T, W), h=torch.ones(T, W), o=torch.ones(T, W), weight=torch.ones(W))
+    with forward_ad.dual_level():
+        t[dual] = forward_ad.make_dual(t[dual], torch.ones_like(t[dual]))
+        with pytest.raises(NotImplementedError, match="forward"):
+            norm.residual_norm_backward(**t)
+
+
+def test_transforms_of_functions_are_refused(calls):
+    t = tensors()
+    with pytest.raises(NotImplementedError, match="forward"):
+        torch.func.jvp(lambda x: norm.residual_norm(x, t["o"]), (t["x"],), (t["x"],))
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda x: norm.residual_norm(x, t["o"]).sum())(t["x"])
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda x: norm.residual_norm(x[None], t["o"][:1]))(t["x"])
+    assert not calls
