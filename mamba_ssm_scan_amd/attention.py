@@ -216,21 +216,32 @@ def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1
     """m3_rope: x [tokens][heads][dim] (bf16 or fp32) turned by positions [tokens] int32; returns out.
 
     backward: the transposed map (dL/dx from x = dL/dy). out may be x itself. stream: the current one unless given.
-    The result takes part in autograd where x does, unless out is given.
+    The result takes part in autograd where x does, unless out is given; an out that requires a gradient itself, or is x
+    where x does, is refused while gradients are recorded. There is no forward-mode derivative.
     """
     dev, dt = _device_of(x, "x"), x.dtype
-    if out is None and x.requires_grad and torch.is_grad_enabled():
-        return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward)
+    _no_tangents("rope", x, inv_freq)
+    if torch.is_grad_enabled():
+        if out is None:
+            if x.requires_grad:
+                return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward)
+        elif isinstance(out, torch.Tensor) and (out.requires_grad or (x.requires_grad and out.numel() > 0
+                                                                      and out.data_ptr() == x.data_ptr())):
+            raise RuntimeError("out takes no part in autograd: it may neither require a gradient nor be x where x does "
+                               "(torch.no_grad() where none is wanted)")
+    given = out is not None
     code = binding._io_code(dt)
     rx = _rows(x, "x", dev, dt)
     shape = x.shape
     T, H, D = shape
     pos = _dense(positions, "positions", dev, torch.int32, (T,))
     rot = _rotary(inv_freq, dev, interleaved, mscale)
-    if out is None:
+    if not given:
         out = x.new_empty(shape)
     ry = _rows(out, "out", dev, dt, shape)
     check(_lib().m3_rope(rx, ry, T, H, D, code, pos, rot, 1 if backward else 0, _handle(dev)))
+    if given:  # what autograd kept of it before is no longer there
+        torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -1,0 +1,67 @@
+"""What rope refuses about gradients, without a GPU: the library call is replaced by one that reports success and writes
+nothing."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from mamba_ssm_scan_amd import attention
+
+T, H, D = 3, 2, 16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = []
+
+    class Library:
+        def m3_rope(self, *args):
+            got.append(args)
+            return 0
+
+    monkeypatch.setattr(attention, "_device_of", lambda t, name: t.device)
+    monkeypatch.setattr(attention, "_handle", lambda device: 0)
+    monkeypatch.setattr(attention, "_lib", Library)
+    return got
+
+
+def inputs():
+    return torch.ones(T, H, D), torch.arange(T, dtype=torch.int32), torch.ones(D // 2)
+
+
+def test_in_place_of_rows_with_a_history(calls):
+    """out = x would keep x's history, of rows that were not turned."""
+    x, pos, f = inputs()
+    leaf = x.clone().requires_grad_()
+    for t in (leaf, leaf * 2):
+        for out in (t, t.detach()):
+            with pytest.raises(RuntimeError, match="out"):
+                attention.rope(t, pos, f, out=out)
+    with pytest.raises(RuntimeError, match="out"):
+        attention.rope(x, pos, f, out=leaf)
+    assert not calls
+    with torch.no_grad():
+        attention.rope(leaf, pos, f, out=leaf)
+    attention.rope(x, pos, f, out=x)
+    assert not attention.rope(leaf, pos, f, out=torch.empty(T, H, D)).requires_grad
+    assert len(calls) == 3
+
+
+def test_rows_that_autograd_kept_and_that_out_overwrites(calls):
+    x, pos, f = inputs()
+    s = torch.ones(D, requires_grad=True)
+    y = (x * s).sum()
+    attention.rope(x, pos, f, out=x)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward()
+
+
+@pytest.mark.parametrize("asked", [False, True])
+def test_forward_mode_is_refused(calls, asked):
+    x, pos, f = inputs()
+    x.requires_grad_(asked)
+    with forward_ad.dual_level():
+        with pytest.raises(NotImplementedError, match="forward"):
+            attention.rope(forward_ad.make_dual(x, torch.ones_like(x)), pos, f)
+        with pytest.raises(NotImplementedError, match="forward"):
+            attention.rope(x, pos, forward_ad.make_dual(f, torch.ones_like(f)))
+    assert not calls
