@@ -34,7 +34,8 @@ typedef struct m3_lines {
  * x and h are the residual stream, in stream_dtype; o, gate and y in io_dtype (of an fp32
  * stream bf16 or fp32, of a bf16 stream bf16). Vectors are fp32 [width]. All arithmetic is
  * fp32, y from h before its rounding; each output is rounded once. Sums of squares are
- * fp32: entries of h and o up to about 2^60.
+ * fp32: entries of h and of a normed o up to 2^60, whole rows of them too (beside an eps of 0 rows of
+ * root mean square 2^-48 at least).
  */
 typedef struct m3_joint {
     int64_t tokens;           /* rows, >= 0 */

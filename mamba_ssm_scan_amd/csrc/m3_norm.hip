@@ -117,6 +117,15 @@ __device__ __forceinline__ void vector8(const float* p, float f, int c, int tid,
     }
 }
 
+// Squares are summed as 2^-6 of themselves, an exact scaling: a full row of 8192 entries of
+// 2^60 stays in range (2^127).
+constexpr float kSquare = 0x1p-6f;
+__device__ __forceinline__ float add_square(float v, float s) { return __builtin_fmaf(v * kSquare, v, s); }
+// 1 / sqrt(mean v^2 + eps) of such a sum
+__device__ __forceinline__ float inverse_rms(float s, float inv_width, float eps) {
+    return __builtin_amdgcn_rsqf(__builtin_fmaf(s, inv_width * (1.f / kSquare), eps));
+}
+
 // Sums over a row's threads, the same bits in each. More than a wave: through LDS, two
 // buffers in turn, so that one barrier a sum is enough.
 template <int TPR, int N>
@@ -208,10 +217,10 @@ __global__ __launch_bounds__(kForwardThreads<TPR>) void joint_kernel(NormDev d) 
                     float o[8];
                     values(now.o[c], o);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) s[0] = __builtin_fmaf(o[k], o[k], s[0]);
+                    for (int k = 0; k < 8; ++k) s[0] = add_square(o[k], s[0]);
                 }
                 row_sum<TPR, 1>(s, lds, turn);
-                r1 = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], d.inv_width, a.j.eps));
+                r1 = inverse_rms(s[0], d.inv_width, a.j.eps);
             }
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -235,9 +244,9 @@ __global__ __launch_bounds__(kForwardThreads<TPR>) void joint_kernel(NormDev d) 
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) s[0] = __builtin_fmaf(h[c][k], h[c][k], s[0]);
+                for (int k = 0; k < 8; ++k) s[0] = add_square(h[c][k], s[0]);
             row_sum<TPR, 1>(s, lds, turn);
-            const float r2 = __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], d.inv_width, a.j.eps));
+            const float r2 = inverse_rms(s[0], d.inv_width, a.j.eps);
             if (row < a.j.tokens) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
@@ -320,15 +329,15 @@ __global__ __launch_bounds__(kNormBackThreads) void joint_back_kernel(NormBackDe
                 values(now.o, o);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    s[0] = __builtin_fmaf(h[k], h[k], s[0]);
+                    s[0] = add_square(h[k], s[0]);
                     s[1] = __builtin_fmaf(dy[k] * hw2[k], h[k], s[1]);
-                    s[2] = __builtin_fmaf(o[k], o[k], s[2]);
+                    s[2] = add_square(o[k], s[2]);
                 }
             }
             row_sum<TPR, 3>(s, lds, turn);
-            r2 = normed ? __builtin_amdgcn_rsqf(__builtin_fmaf(s[0], d.inv_width, a.j.eps)) : 0.f;
+            r2 = normed ? inverse_rms(s[0], d.inv_width, a.j.eps) : 0.f;
             back = s[1] * r2 * d.inv_width * r2;
-            if (post) r1 = __builtin_amdgcn_rsqf(__builtin_fmaf(s[2], d.inv_width, a.j.eps));
+            if (post) r1 = inverse_rms(s[2], d.inv_width, a.j.eps);
         }
         // the stream's gradient, and the branch's parts: act, slope, v
         float t[8], act[8], slope[8], n1[8];
