@@ -200,15 +200,20 @@ class _Rope(torch.autograd.Function):
     """rope as a step of autograd: linear, with the transposed map as its gradient."""
 
     @staticmethod
-    def forward(ctx, x, positions, inv_freq, interleaved, mscale, backward):
+    def forward(ctx, x, positions, inv_freq, interleaved, mscale, backward, in_place):
         ctx.save_for_backward(positions, inv_freq)
         ctx.how = dict(interleaved=interleaved, mscale=mscale, backward=not backward)
-        return rope(x.detach(), positions, inv_freq, interleaved=interleaved, mscale=mscale, backward=backward)
+        if in_place:
+            ctx.mark_dirty(x)
+        rows = x.detach()
+        y = rope(rows, positions, inv_freq, out=rows if in_place else None, interleaved=interleaved, mscale=mscale,
+                 backward=backward)
+        return x if in_place else y
 
     @staticmethod
     def backward(ctx, dy):
         dy = dy if dy.stride(-1) == 1 or dy.shape[-1] == 1 else dy.contiguous()
-        return rope(dy, *ctx.saved_tensors, **ctx.how), None, None, None, None, None
+        return rope(dy, *ctx.saved_tensors, **ctx.how), None, None, None, None, None, None
 
 
 @_on_stream
@@ -216,19 +221,18 @@ def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1
     """m3_rope: x [tokens][heads][dim] (bf16 or fp32) turned by positions [tokens] int32; returns out.
 
     backward: the transposed map (dL/dx from x = dL/dy). out may be x itself. stream: the current one unless given.
-    The result takes part in autograd where x does, unless out is given; an out that requires a gradient itself, or is x
-    where x does, is refused while gradients are recorded. There is no forward-mode derivative.
+    The result takes part in autograd where x does, unless an out other than x is given (one that requires a gradient is
+    refused while gradients are recorded, as is a leaf in place). There is no forward-mode derivative.
     """
     dev, dt = _device_of(x, "x"), x.dtype
     _no_tangents("rope", x, inv_freq)
     if torch.is_grad_enabled():
-        if out is None:
-            if x.requires_grad:
-                return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward)
-        elif isinstance(out, torch.Tensor) and (out.requires_grad or (x.requires_grad and out.numel() > 0
-                                                                      and out.data_ptr() == x.data_ptr())):
-            raise RuntimeError("out takes no part in autograd: it may neither require a gradient nor be x where x does "
-                               "(torch.no_grad() where none is wanted)")
+        if x.requires_grad and (out is None or out is x):
+            if out is x and (x.is_leaf or (x._base is not None and x._base.is_leaf)):
+                raise RuntimeError("a leaf that requires a gradient cannot be turned in place")
+            return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward, out is x)
+        if isinstance(out, torch.Tensor) and out.requires_grad:
+            raise RuntimeError("an out other than x takes no part in autograd: it may not require a gradient")
     given = out is not None
     code = binding._io_code(dt)
     rx = _rows(x, "x", dev, dt)

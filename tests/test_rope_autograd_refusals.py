@@ -1,4 +1,4 @@
-"""What rope refuses about gradients, without a GPU: the library call is replaced by one that reports success and writes
+"""What rope does about gradients in place, and what it refuses, without a GPU: the library call is replaced by one that reports success and writes
 nothing."""
 import pytest
 import torch
@@ -28,16 +28,33 @@ def inputs():
     return torch.ones(T, H, D), torch.arange(T, dtype=torch.int32), torch.ones(D // 2)
 
 
-def test_in_place_of_rows_with_a_history(calls):
-    """out = x would keep x's history, of rows that were not turned."""
+def test_in_place_is_a_step_of_autograd(calls):
+    """out = x kept x's history, of rows that were not turned. (The replaced call turns nothing, forward or backward.)"""
     x, pos, f = inputs()
     leaf = x.clone().requires_grad_()
-    for t in (leaf, leaf * 2):
-        for out in (t, t.detach()):
-            with pytest.raises(RuntimeError, match="out"):
-                attention.rope(t, pos, f, out=out)
-    with pytest.raises(RuntimeError, match="out"):
-        attention.rope(x, pos, f, out=leaf)
+    for t in (leaf * 2, (leaf * 2).view(T, H, D), (leaf.view(T, 2 * D) * 2).view(T, H, D)):
+        before = t._version
+        assert attention.rope(t, pos, f, out=t) is t
+        assert t._version > before
+        n = len(calls)
+        torch.autograd.grad(t.sum(), leaf)
+        assert len(calls) == n + 1                           # (the gradient passed through the transposed map)
+    square = leaf * 2
+    kept = square.square().sum()
+    attention.rope(square, pos, f, out=square)
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.backward()
+
+
+def test_out_that_autograd_would_misread(calls):
+    x, pos, f = inputs()
+    leaf = x.clone().requires_grad_()
+    for t in (leaf, leaf[:], leaf.view(T, H, D)):
+        with pytest.raises(RuntimeError, match="leaf"):
+            attention.rope(t, pos, f, out=t)
+    for out in (leaf, leaf * 2):
+        with pytest.raises(RuntimeError, match="out"):
+            attention.rope(x, pos, f, out=out)
     assert not calls
     with torch.no_grad():
         attention.rope(leaf, pos, f, out=leaf)
