@@ -204,7 +204,8 @@ typedef struct m3_kv_view {
 /*
  * m3_kv_attend_view -- m3_kv_attend over such a view. The outputs are those of m3_kv_attend over tables that name
  * the shared pages themselves (up to the order of fp32 sums); the prefix of a group is read once
- * for many of its rows where that pays.
+ * for many of its rows where that pays, without a window and up to 64 (row, head of a group)
+ * pairs a sequence (32 for fp32 rows and above headdim 128). Sequences with more rows each read it for their own.
  */
 m3_status m3_kv_attend_view(const m3_kv_cache* cache, const m3_kv_batch* batch, const m3_kv_view* view,
                             const m3_rows* q, void* out, float* lse, int32_t q_heads, m3_dtype io_dtype, float scale,

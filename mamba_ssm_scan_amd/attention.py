@@ -257,7 +257,8 @@ class SharedPrefix:
     group of the whole batch). The sequences' positions, lengths and own page tables count the prefix as ever; their
     own entries for its pages are not read. A sequence outside every group shares nothing. The tensors' contents may
     change between calls; other tensors are another SharedPrefix. A launch is sized by the table's width: one much wider than the
-    prefixes costs time.
+    prefixes costs time (64 steps behind 512 tokens 2.4 times as much). The pages are read once for many sequences' rows only without a window and
+    while a sequence has up to 64 (row, head of a group) pairs (32 for fp32 rows and above headdim 128).
     """
 
     def __init__(self, pages, count, cu_seqs=None):

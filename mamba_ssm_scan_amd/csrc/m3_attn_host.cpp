@@ -296,7 +296,8 @@ static AttendPlan parts_plan(AttendPlan p, const m3_kv_cache& c, const m3_kv_bat
 
 // Parts where they save enough, by what the prefix takes either way (us; from measurements). A wave's pass of up to 16 rows
 // over a tile of 64 keys at headdim 128 takes 1 / 358 of the chip (32 rows: 1.4 times that), a pass of 128 rows in the
-// kernel for many rows 1 / 136 (256 rows: 1.6 times); passes of fp32 rows half as much again. Parts of
+// kernel for many rows 1 / 136 (256 rows: 1.6 times); passes of fp32 rows half as much again (that and the factors
+// of other headdims are set by the size of the products, not fitted). Parts of
 // their own cost 3 more where the one pass deals out shares and joins anyway, else 10, the launch for many rows 10 to
 // 12 on top. 16 heads over 4 of 128, parts and one pass, behind 512 tokens 16 / 64 sequences 17 / 24 us and 15 / 17;
 // behind 2048 8 / 16 / 64 / 128 of them 17 / 18 / 29 / 35 and 16 / 23 / 37 / 44; behind 8192 2 / 4 / 16 / 128 of them 18

@@ -7,15 +7,21 @@
 //   v = dx m                               dw1 = sum v n1,  ds = sum dx a(g) N(o)
 //   do = r1 (v w1 - n1 mean(v w1 n1))      dg = dx s a'(g) N(o)
 //
-// Bound by memory: every row is read and written once and held in registers in between, 8
-// entries a thread (16 bytes of bf16), so that a row belongs to 16 .. 1024 threads and a
-// sum over it takes a butterfly in each wave and one exchange through LDS. The vectors stay
-// in registers over a workgroup's rows, and the next row's loads are issued before this
-// row's sums. 8192 rows of 2048, all parts: forward with an fp32 stream 43 us (5.4 TB/s), backward
-// in bf16 53 + 4 us for the joining of its sums (5.0 TB/s); 16384 of 4096, fp32 stream: 174 and
-// 269 + 4 us (5.4 and 5.5 TB/s); one step of 128 rows 3.5 us, a launch's least. Rows that are not
-// 16-byte aligned (1999 of 1283, fp32): 23 + 4 us at 3.5 TB/s, entry by entry; 16-byte loads at any
-// alignment took 31 us, as the hardware splits them.
+// Bound by memory. Up to width 4096 every row is read and written once and held in registers
+// in between, 8 entries a thread (16 bytes of bf16), so that a row belongs to 16 .. 512 threads
+// and a sum over it takes a butterfly in each wave and one exchange through LDS. The vectors
+// stay in registers over a workgroup's rows, and the next row's loads are issued before this
+// row's sums. 8192 rows of 2048, all parts: forward with an fp32 stream 45 to 49 us (4.8 to 5.2 TB/s),
+// backward in bf16 54 + 4 us for the joining of its sums (5.0 TB/s); 16384 of 4096, fp32 stream: 174
+// and 269 + 4 us (5.4 and 5.5 TB/s); one step of 128 rows 3.5 us, a launch's least.
+//   Above 4096 a row's loads wait for the row before: the forward pass has 1024 threads a row, the
+// backward pass 16 entries a thread, and reads each row up to three times. 8192 rows, all parts,
+// bytes of one read: width 8192, bf16 156 and 385 us (4.3 and 2.8 TB/s), fp32 stream 182 and 449, fp32 250
+// and 607; width 5120, whose last threads idle, bf16 126 and 298 (3.3 and 2.3).
+//   Rows that are not 16-byte aligned go entry by entry: 1999 of 1283, fp32, backward 23 + 4 us at 3.5 TB/s
+// (16-byte loads at any alignment took 31 us, as the hardware splits them); through the calls, forward
+// and backward, 15 and 30 us, in bf16, whose entries are half as wide, 13 and 31. Worst above 4096: 8192 rows of
+// 8191 in bf16 176 us and 2.06 ms.
 #include <algorithm>
 
 #include "m3_attn_device.h"
@@ -172,7 +178,7 @@ constexpr int kForwardThreads = TPR < 256 ? 256 : TPR;
 template <typename X, typename T, int TPR, int CH, bool WIDE>
 __global__ __launch_bounds__(kForwardThreads<TPR>) void joint_kernel(NormDev d) {
     constexpr int NT = kForwardThreads<TPR>, RPW = NT / TPR;
-    constexpr bool kAhead = TPR <= 512;  // (1024 threads have 128 registers)
+    constexpr bool kAhead = TPR <= 512;  // (above width 4096 a row is loaded after the one before)
     __shared__ float lds[2][1024 / 64][3];
     const NormArgs& a = d.a;
     const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR, width = a.j.width;
