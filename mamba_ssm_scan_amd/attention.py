@@ -196,6 +196,16 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: Optional[str] 
     return f.to(torch.float32).to(device), mscale
 
 
+def _may_change(x) -> bool:
+    """Whether autograd lets a step change these rows, which have a history, in place (found out before they are changed)."""
+    if x.is_leaf:
+        return False
+    if x._base is None:
+        return True
+    meta = torch._C._autograd
+    return not x._base.is_leaf and meta._get_creation_meta(x) == meta.CreationMeta.DEFAULT
+
+
 class _Rope(torch.autograd.Function):
     """rope as a step of autograd: linear, with the transposed map as its gradient."""
 
@@ -222,14 +232,16 @@ def rope(x, positions, inv_freq, *, interleaved: bool = False, mscale: float = 1
 
     backward: the transposed map (dL/dx from x = dL/dy). out may be x itself. stream: the current one unless given.
     The result takes part in autograd where x does, unless an out other than x is given (one that requires a gradient is
-    refused while gradients are recorded, as is a leaf in place). There is no forward-mode derivative.
+    refused while gradients are recorded, as is in place what torch does not let change there: leaves, and the views that
+    split and unbind return). There is no forward-mode derivative.
     """
     dev, dt = _device_of(x, "x"), x.dtype
     _no_tangents("rope", x, inv_freq)
     if torch.is_grad_enabled():
         if x.requires_grad and (out is None or out is x):
-            if out is x and (x.is_leaf or (x._base is not None and x._base.is_leaf)):
-                raise RuntimeError("a leaf that requires a gradient cannot be turned in place")
+            if out is x and not _may_change(x):
+                raise RuntimeError("a leaf that requires a gradient, or one of the views that split or unbind returns, "
+                                   "cannot be turned in place while gradients are recorded")
             return _Rope.apply(x, positions, inv_freq, interleaved, mscale, backward, out is x)
         if isinstance(out, torch.Tensor) and out.requires_grad:
             raise RuntimeError("an out other than x takes no part in autograd: it may not require a gradient")
@@ -257,8 +269,9 @@ class SharedPrefix:
     group of the whole batch). The sequences' positions, lengths and own page tables count the prefix as ever; their
     own entries for its pages are not read. A sequence outside every group shares nothing. The tensors' contents may
     change between calls; other tensors are another SharedPrefix. A launch is sized by the table's width: one much wider than the
-    prefixes costs time (64 steps behind 512 tokens 2.4 times as much). The pages are read once for many sequences' rows only without a window and
-    while a sequence has up to 64 (row, head of a group) pairs (32 for fp32 rows and above headdim 128).
+    prefixes costs time (64 steps behind 512 tokens 2.4 times as much). The pages are read once for many sequences' rows
+    only without a window and while a sequence has up to 64 (row, head of a group) pairs (32 for fp32 rows and above
+    headdim 128).
     """
 
     def __init__(self, pages, count, cu_seqs=None):

@@ -49,7 +49,8 @@ def test_in_place_is_a_step_of_autograd(calls):
 def test_out_that_autograd_would_misread(calls):
     x, pos, f = inputs()
     leaf = x.clone().requires_grad_()
-    for t in (leaf, leaf[:], leaf.view(T, H, D)):
+    both = torch.cat([leaf, leaf]) * 2
+    for t in (leaf, leaf[:], leaf.view(T, H, D), both.split(T)[0], both.unflatten(0, (2, T)).unbind(0)[1], both.chunk(2)[1][:]):
         with pytest.raises(RuntimeError, match="leaf"):
             attention.rope(t, pos, f, out=t)
     for out in (leaf, leaf * 2):
